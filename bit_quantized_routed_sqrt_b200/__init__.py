@@ -22,6 +22,9 @@ FLAG_PROFILE = 0x4
 FLAG_TRACE = 0x8
 FLAG_TEST_TIMEOUT = 0x10
 ROUTE_STATIC_MAX_TOKENS = 256
+F32, BF16, F16, MXFP4 = 0, 1, 2, 3
+SCORES = {"softmax": 0, "sigmoid": 1, "sqrt_softplus": 2}
+GROUP_SCORES = {"max": 0, "top2": 1}
 
 STATUS = {0: "DS4MOE_OK", 1: "DS4MOE_EINVAL", 2: "DS4MOE_ENOMEM", 3: "DS4MOE_ECUDA",
           4: "DS4MOE_ESTATE", 5: "DS4MOE_ETIMEOUT", 6: "DS4MOE_EDEVICE"}
@@ -35,6 +38,15 @@ class ds4moe_config(C.Structure):
     _fields_ = [("hidden", C.c_int32), ("n_experts", C.c_int32), ("top_k", C.c_int32),
                 ("inter", C.c_int32), ("shared_inter", C.c_int32), ("max_tokens", C.c_int32),
                 ("flags", C.c_uint32)]
+
+
+class ds4moe_router(C.Structure):
+    _fields_ = [("n_experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32), ("n_groups", C.c_int32),
+                ("topk_groups", C.c_int32), ("group_score", C.c_int32), ("renormalise", C.c_int32), ("scale", C.c_float)]
+
+
+class ds4moe_mxfp4_config(C.Structure):
+    _fields_ = [("n_experts", C.c_int32), ("n_out", C.c_int32), ("n_in", C.c_int32), ("gated", C.c_int32)]
 
 
 class ds4moe_stats(C.Structure):
@@ -62,6 +74,24 @@ lib.ds4moe_status_string.argtypes = [C.c_int]
 lib.ds4moe_status_string.restype = C.c_char_p
 lib.ds4moe_last_error.argtypes = [_vp]
 lib.ds4moe_last_error.restype = C.c_char_p
+_i64, _sz = C.c_int64, C.c_size_t
+lib.ds4moe_route_logits_workspace.argtypes = [C.POINTER(ds4moe_router), _i32]
+lib.ds4moe_route_logits_workspace.restype = _sz
+lib.ds4moe_route_logits.argtypes = [C.POINTER(ds4moe_router), _vp, _i32, _i64, _i32] + [_vp] * 8 + [_sz, _vp]
+lib.ds4moe_mxfp4_quantize.argtypes = [_vp, _i32, _i64, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp]
+lib.ds4moe_mxfp4_dequantize.argtypes = [_vp, _vp, _i32, _i32, _vp, _i32, _i64, _vp]
+lib.ds4moe_combine.argtypes = [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp]
+lib.ds4moe_mxfp4_create.argtypes = [C.POINTER(ds4moe_mxfp4_config), C.c_int, C.POINTER(_vp)]
+lib.ds4moe_mxfp4_destroy.argtypes = [_vp]
+lib.ds4moe_mxfp4_destroy.restype = None
+lib.ds4moe_mxfp4_load.argtypes = [_vp] * 6
+lib.ds4moe_mxfp4_product.argtypes = [_vp, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _vp]
+lib.ds4moe_mxfp4_sync_status.argtypes = [_vp]
+lib.ds4moe_mxfp4_last_error.argtypes = [_vp]
+lib.ds4moe_mxfp4_last_error.restype = C.c_char_p
+for _n in ("ds4moe_route_logits", "ds4moe_mxfp4_quantize", "ds4moe_mxfp4_dequantize", "ds4moe_combine", "ds4moe_mxfp4_create",
+           "ds4moe_mxfp4_load", "ds4moe_mxfp4_product", "ds4moe_mxfp4_sync_status"):
+    getattr(lib, _n).restype = C.c_int
 for _n in ("ds4moe_create", "ds4moe_load_q2k_experts", "ds4moe_route", "ds4moe_route_static", "ds4moe_forward", "ds4moe_forward_host",
            "ds4moe_rms_renorm", "ds4moe_score_eval", "ds4moe_export_q2k", "ds4moe_sync_status", "ds4moe_get_stats",
            "ds4moe_get_trace"):
@@ -105,6 +135,332 @@ def ds4moe_rms_renorm(y, T: int, H: int, x_out, stream=None):
 
 def ds4moe_score_eval(logits, n: int, scores, variant: int = 0, stream=None):
     _check(lib.ds4moe_score_eval(_ptr(logits), n, _ptr(scores), variant, _stream(stream)), None, "ds4moe_score_eval")
+
+
+# -- operators beside the layer ------------------------------------------------------
+# The ds4moe_* functions take what the C calls take (tensors or addresses); the classes and the
+# functions below them read types, sizes and the device from torch tensors and refuse, with a
+# ValueError, tensors of another type, shape, layout or device than the call needs.
+
+def ds4moe_route_logits_workspace(router: ds4moe_router, T: int) -> int:
+    return lib.ds4moe_route_logits_workspace(C.byref(router), T)
+
+
+def ds4moe_route_logits(router: ds4moe_router, logits, logits_type, ld, T, bias, topk_idx, topk_w, offsets=None,
+                        sorted_token=None, sorted_slot=None, inv_pos=None, workspace=None, workspace_bytes=0, stream=None):
+    _check(lib.ds4moe_route_logits(C.byref(router), _ptr(logits), logits_type, ld, T, _ptr(bias), _ptr(topk_idx),
+                                   _ptr(topk_w), _ptr(offsets), _ptr(sorted_token), _ptr(sorted_slot), _ptr(inv_pos),
+                                   _ptr(workspace), workspace_bytes, _stream(stream)), None, "ds4moe_route_logits")
+
+
+def ds4moe_mxfp4_quantize(x, x_type, ld, rows, K, inv_pos, top_k, out_rows, codes, scales, stream=None):
+    _check(lib.ds4moe_mxfp4_quantize(_ptr(x), x_type, ld, rows, K, _ptr(inv_pos), top_k, out_rows, _ptr(codes),
+                                     _ptr(scales), _stream(stream)), None, "ds4moe_mxfp4_quantize")
+
+
+def ds4moe_mxfp4_dequantize(codes, scales, rows, K, out, out_type, ld, stream=None):
+    _check(lib.ds4moe_mxfp4_dequantize(_ptr(codes), _ptr(scales), rows, K, _ptr(out), out_type, ld, _stream(stream)),
+           None, "ds4moe_mxfp4_dequantize")
+
+
+def ds4moe_combine(o, o_type, o_rows, T, top_k, H, inv_pos, topk_w, add, add_type, y, y_type, stream=None):
+    _check(lib.ds4moe_combine(_ptr(o), o_type, o_rows, T, top_k, H, _ptr(inv_pos), _ptr(topk_w), _ptr(add), add_type,
+                              _ptr(y), y_type, _stream(stream)), None, "ds4moe_combine")
+
+
+def _check_mxfp4(rc: int, handle, what: str):
+    if rc != 0:
+        detail = lib.ds4moe_mxfp4_last_error(handle).decode() if handle else ""
+        raise Ds4MoeError("%s failed: %s (%s) %s" % (what, STATUS.get(rc, rc),
+                                                   lib.ds4moe_status_string(rc).decode(), detail))
+
+
+def ds4moe_mxfp4_create(cfg: ds4moe_mxfp4_config, device: int) -> int:
+    h = _vp()
+    _check_mxfp4(lib.ds4moe_mxfp4_create(C.byref(cfg), device, C.byref(h)), None, "ds4moe_mxfp4_create")
+    return h
+
+
+def ds4moe_mxfp4_destroy(handle):
+    lib.ds4moe_mxfp4_destroy(handle)
+
+
+def ds4moe_mxfp4_load(handle, codes, scales, up_codes=None, up_scales=None, stream=None):
+    _check_mxfp4(lib.ds4moe_mxfp4_load(handle, _ptr(codes), _ptr(scales), _ptr(up_codes), _ptr(up_scales),
+                                       _stream(stream)), handle, "ds4moe_mxfp4_load")
+
+
+def ds4moe_mxfp4_product(handle, a_codes, a_scales, rows, offsets, out, out_type, ld, out_scales=None, stream=None):
+    _check_mxfp4(lib.ds4moe_mxfp4_product(handle, _ptr(a_codes), _ptr(a_scales), rows, _ptr(offsets), _ptr(out), out_type,
+                                          ld, _ptr(out_scales), _stream(stream)), handle, "ds4moe_mxfp4_product")
+
+
+def ds4moe_mxfp4_sync_status(handle):
+    _check_mxfp4(lib.ds4moe_mxfp4_sync_status(handle), handle, "ds4moe_mxfp4_sync_status")
+
+
+def ds4moe_mxfp4_last_error(handle) -> str:
+    return lib.ds4moe_mxfp4_last_error(handle).decode()
+
+
+_TYPES = {"torch.float32": F32, "torch.bfloat16": BF16, "torch.float16": F16}
+_type_codes = {}
+
+
+def _type_of(t, what: str) -> int:
+    c = _type_codes.get(t.dtype)
+    if c is None:
+        c = _type_codes[t.dtype] = _TYPES.get(str(t.dtype), -1)
+    if c < 0:
+        raise ValueError("%s must be float32, bfloat16 or float16, not %s" % (what, t.dtype))
+    return c
+
+
+def _rows_of(t, what: str):
+    """(rows, width, elements between rows) of a matrix whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions" % what)
+    rows, width = t.shape
+    ld = t.stride(0) if rows > 1 else width
+    if (width > 1 and t.stride(1) != 1) or ld < width:
+        raise ValueError("%s must have contiguous rows, one behind the other" % what)
+    return rows, width, ld
+
+
+def _flat(t, dtype: str, n: int, what: str, device):
+    """t as a contiguous tensor of n elements of the type on the device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not _torch_dtypes()[dtype] or t.numel() != n or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous %s tensor of %d elements on %s" % (what, dtype, n, device))
+    return t
+
+
+_dtypes = {}
+
+
+def _torch_dtypes():
+    if not _dtypes:
+        import torch
+        _dtypes.update(int32=torch.int32, uint8=torch.uint8, float32=torch.float32)
+    return _dtypes
+
+
+class _on:
+    """The tensor's device as the current one for a call, and its current stream's address."""
+
+    def __init__(self, t, what: str):
+        if not t.is_cuda:
+            raise ValueError("%s must be on a CUDA device" % what)
+        import torch
+        self.device = t.device
+        self.index = t.device.index
+        self.torch = torch
+
+    def __enter__(self):
+        self.before = self.torch.cuda.current_device()
+        if self.before != self.index:
+            self.torch.cuda.set_device(self.index)
+        return self.torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            self.torch.cuda.set_device(self.before)
+
+
+class Routing:
+    """Outputs and workspace of Router.route for T tokens (Router.buffers)."""
+
+    def __init__(self, router: "Router", T: int, device):
+        import torch
+        k, E = router.cfg.top_k, router.cfg.n_experts
+        self.T = T
+        self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=device)
+        self.topk_w = torch.empty((T, k), dtype=torch.float32, device=device)
+        self.expert_offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
+        self.sorted_token = torch.empty(T * k, dtype=torch.int32, device=device)
+        self.sorted_slot = torch.empty(T * k, dtype=torch.int32, device=device)
+        self.inv_pos = torch.empty(T * k, dtype=torch.int32, device=device)
+        n = ds4moe_route_logits_workspace(router.cfg, T)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+class Router:
+    """How experts are chosen and weighted (``ds4moe_router``), applied to router logits."""
+
+    def __init__(self, n_experts: int, top_k: int, score: str = "softmax", n_groups: int = 1, topk_groups: int = 1,
+                 group_score: str = "max", renormalise: bool = True, scale: float = 1.0):
+        if score not in SCORES or group_score not in GROUP_SCORES:
+            raise ValueError("score must be one of %s, group_score of %s" % (sorted(SCORES), sorted(GROUP_SCORES)))
+        self.cfg = ds4moe_router(n_experts, top_k, SCORES[score], n_groups, topk_groups, GROUP_SCORES[group_score],
+                                 int(bool(renormalise)), scale)
+
+    def buffers(self, T: int, device="cuda") -> Routing:
+        return Routing(self, T, device)
+
+    def route(self, logits, bias=None, out: Optional[Routing] = None) -> Routing:
+        """Routes the rows of logits [T, E] (rows may be strided); out: buffers of T tokens to write to."""
+        T, E, ld = _rows_of(logits, "logits")
+        on = _on(logits, "logits")
+        code = _type_of(logits, "logits")
+        if E != self.cfg.n_experts:
+            raise ValueError("logits have %d columns for %d experts" % (E, self.cfg.n_experts))
+        _flat(bias, "float32", E, "bias", on.device)
+        if out is None:
+            out = Routing(self, T, on.device)
+        elif out.T != T or out.topk_idx.shape[1] != self.cfg.top_k or out.expert_offsets.numel() != E + 1 or \
+                out.topk_idx.device != on.device:
+            raise ValueError("out holds buffers of another size or device")
+        ws = out.workspace
+        with on as stream:
+            ds4moe_route_logits(self.cfg, logits, code, ld, T, bias, out.topk_idx, out.topk_w, out.expert_offsets,
+                                out.sorted_token, out.sorted_slot, out.inv_pos, ws, 0 if ws is None else ws.numel(),
+                                stream)
+        return out
+
+
+def mxfp4_quantize(x, inv_pos=None, codes=None, scales=None):
+    """(codes, scales) of the rows of x; with inv_pos [rows, k] (int32) row r goes to rows inv_pos[r, j]
+    of codes / scales (rows * k of them where they are not given)."""
+    import torch
+    rows, K, ld = _rows_of(x, "x")
+    on = _on(x, "x")
+    code = _type_of(x, "x")
+    if K == 0 or K % 32:
+        raise ValueError("the rows of x must have a multiple of 32 elements")
+    k = 1
+    if inv_pos is not None:
+        if inv_pos.dim() != 2 or inv_pos.shape[0] != rows:
+            raise ValueError("inv_pos must have a row for each row of x")
+        k = inv_pos.shape[1]
+        _flat(inv_pos, "int32", rows * k, "inv_pos", on.device)
+    if codes is None:
+        codes = torch.empty((rows * k, K // 2), dtype=torch.uint8, device=x.device)
+    out_rows = codes.shape[0]
+    if scales is None:
+        scales = torch.empty((out_rows, K // 32), dtype=torch.uint8, device=x.device)
+    _flat(codes, "uint8", out_rows * (K // 2), "codes", on.device)
+    _flat(scales, "uint8", out_rows * (K // 32), "scales", on.device)
+    with on as stream:
+        ds4moe_mxfp4_quantize(x, code, ld, rows, K, inv_pos, k, out_rows, codes, scales, stream)
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, out=None):
+    """The values of MXFP4 rows, in out (float32, bfloat16 or float16 [rows, K]; bfloat16 where it is not given,
+    which holds every value but 2^-127 * 0.5 exactly)."""
+    import torch
+    rows, half, _ = _rows_of(codes, "codes")
+    K = 2 * half
+    on = _on(codes, "codes")
+    _flat(codes, "uint8", rows * half, "codes", on.device)
+    _flat(scales, "uint8", rows * (K // 32), "scales", on.device)
+    if out is None:
+        out = torch.empty((rows, K), dtype=torch.bfloat16, device=codes.device)
+    r, w, ld = _rows_of(out, "out")
+    if (r, w) != (rows, K) or out.device != on.device:
+        raise ValueError("out must be [%d, %d] on %s" % (rows, K, on.device))
+    with on as stream:
+        ds4moe_mxfp4_dequantize(codes, scales, rows, K, out, _type_of(out, "out"), ld, stream)
+    return out
+
+
+def combine(o, inv_pos, topk_w, y=None, add=None):
+    """y[t] = add[t] + sum_j topk_w[t, j] * o[inv_pos[t, j]] (a row outside o adds nothing); y is float32 where it
+    is not given."""
+    import torch
+    o_rows, H, ld = _rows_of(o, "o")
+    on = _on(o, "o")
+    if ld != H:
+        raise ValueError("o must be contiguous")
+    if topk_w.dim() != 2:
+        raise ValueError("topk_w must be [T, k]")
+    T, k = topk_w.shape
+    _flat(topk_w, "float32", T * k, "topk_w", on.device)
+    _flat(inv_pos, "int32", T * k, "inv_pos", on.device)
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.float32, device=o.device)
+    for t, what in ((y, "y"), (add, "add")):
+        if t is not None and (tuple(t.shape) != (T, H) or not t.is_contiguous() or t.device != on.device):
+            raise ValueError("%s must be a contiguous [%d, %d] tensor on %s" % (what, T, H, on.device))
+    with on as stream:
+        ds4moe_combine(o, _type_of(o, "o"), o_rows, T, k, H, inv_pos, topk_w, add,
+                       0 if add is None else _type_of(add, "add"), y, _type_of(y, "y"), stream)
+    return y
+
+
+class Mxfp4Experts:
+    """One projection of E experts in MXFP4 (the ``ds4moe_mxfp4`` handle): W [E, n_out, n_in], or a gate and an up
+    matrix whose product is silu(gate x) * (up x)."""
+
+    def __init__(self, n_experts: int, n_out: int, n_in: int, gated: bool = False, device: Optional[int] = None):
+        if device is None:
+            import torch
+            device = torch.cuda.current_device()
+        self.h = None
+        self.n_experts, self.n_out, self.n_in, self.gated = n_experts, n_out, n_in, bool(gated)
+        self.h = ds4moe_mxfp4_create(ds4moe_mxfp4_config(n_experts, n_out, n_in, int(self.gated)), device)
+        self.device = device
+
+    def close(self):
+        if getattr(self, "h", None):
+            ds4moe_mxfp4_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _on(self, t, what):
+        on = _on(t, what)
+        if on.index != self.device:
+            raise ValueError("%s is on %s, the experts on device %d" % (what, on.device, self.device))
+        return on
+
+    def load(self, codes, scales, up_codes=None, up_scales=None):
+        """codes uint8 [E, n_out, n_in / 2] and scales uint8 [E, n_out, n_in / 32] on the device; a gated projection
+        takes the gate's and the up matrix's."""
+        if (up_codes is None) != (up_scales is None) or (up_codes is not None) != self.gated:
+            raise ValueError("a gated projection takes two matrices, another takes one")
+        on = self._on(codes, "codes")
+        n = self.n_experts * self.n_out
+        for t, per, what in ((codes, self.n_in // 2, "codes"), (scales, self.n_in // 32, "scales"),
+                             (up_codes, self.n_in // 2, "up_codes"), (up_scales, self.n_in // 32, "up_scales")):
+            _flat(t, "uint8", n * per, what, on.device)
+        with on as stream:
+            ds4moe_mxfp4_load(self.h, codes, scales, up_codes, up_scales, stream)
+
+    def product(self, a_codes, a_scales, offsets=None, out=None, out_scales=None):
+        """Rows of a [rows, n_in] in MXFP4, grouped by offsets int32 [E + 1] (None for one expert), times their
+        experts' matrices.  out: [rows, n_out] of float32, bfloat16 (where it is not given) or float16, rows may be
+        strided; or uint8 [rows, n_out / 2] with out_scales uint8 [rows, n_out / 32] for MXFP4."""
+        import torch
+        rows, half, _ = _rows_of(a_codes, "a_codes")
+        on = self._on(a_codes, "a_codes")
+        if half * 2 != self.n_in:
+            raise ValueError("a_codes has rows of %d inputs, the experts take %d" % (half * 2, self.n_in))
+        _flat(a_codes, "uint8", rows * half, "a_codes", on.device)
+        _flat(a_scales, "uint8", rows * (self.n_in // 32), "a_scales", on.device)
+        _flat(offsets, "int32", self.n_experts + 1, "offsets", on.device)
+        if out is None:
+            out = torch.empty((rows, self.n_out), dtype=torch.bfloat16, device=a_codes.device)
+        if out_scales is not None:
+            _flat(out, "uint8", rows * (self.n_out // 2), "out", on.device)
+            _flat(out_scales, "uint8", rows * (self.n_out // 32), "out_scales", on.device)
+            code, ld = MXFP4, self.n_out
+        else:
+            r, n, ld = _rows_of(out, "out")
+            if (r, n) != (rows, self.n_out) or out.device != on.device:
+                raise ValueError("out must be [%d, %d] on %s" % (rows, self.n_out, on.device))
+            code = _type_of(out, "out")
+        with on as stream:
+            ds4moe_mxfp4_product(self.h, a_codes, a_scales, rows, offsets, out, code, ld, out_scales, stream)
+        return out
+
+    def sync_status(self):
+        ds4moe_mxfp4_sync_status(self.h)
 
 
 class Ds4Moe:

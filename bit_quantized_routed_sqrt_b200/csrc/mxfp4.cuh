@@ -1,0 +1,200 @@
+// mxfp4.cuh -- MXFP4 rows: quantisation, dequantisation and the packed layout of weights.
+//
+// MXFP4 (the OCP microscaling format): 32 consecutive inputs of a row share one scale byte s
+// (E8M0, the value 2^(s - 127); 255 is NaN) and are E2M1 codes: sign bit, then the index of
+// one of 0, 0.5, 1, 1.5, 2, 3, 4, 6.  Element 2i of a row is the low nibble of code byte i.
+#pragma once
+#include "common.cuh"
+
+namespace ds4 {
+
+constexpr int MX_BLOCK = 32;        // inputs that share a scale
+
+enum : int { DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2, DT_MXFP4 = 3 };
+
+// The value of a scale byte in fp32 (2^-127 is a subnormal).
+__device__ __forceinline__ float e8m0_value(uint32_t s) {
+    return __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
+}
+// Two codes (low nibble first) -> two fp16 values, exactly.
+__device__ __forceinline__ __half2 e2m1x2_value(uint32_t byte) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(byte));
+    return *reinterpret_cast<__half2 *>(&r);
+}
+// Two fp32 values -> codes (lo in the low nibble), nearest even, saturated at +-6.
+__device__ __forceinline__ uint32_t e2m1x2_code(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+    return r & 0xFFu;
+}
+
+// The scale byte of a block from the largest |x| of it, as fp32 bits: the exponent of the
+// largest magnitude less 2 (6 is the largest E2M1 value, 4 its power of two), at least -127.
+// A block that holds a NaN or an infinity gets the NaN scale.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+    if (amax_bits >= 0x7f800000u) return 255u;
+    const int e = (int)(amax_bits >> 23);   // a subnormal's 0 ends below 2 as well
+    return e > 2 ? (uint32_t)(e - 2) : 0u;
+}
+// 2^-(s - 127) for a scale byte 0..252: exact, so x times it is x over the scale.
+__device__ __forceinline__ float mx_inverse(uint32_t s) { return __uint_as_float((254u - s) << 23); }
+
+// ------------------------------------------------------------------ row types
+template <class T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <class T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// N consecutive values, N * sizeof(T) a multiple of 16 and p 16-byte aligned, or one by one.
+template <class T, int N, bool VEC>
+__device__ __forceinline__ void load_row(const T *p, float (&v)[N]) {
+    if (VEC) {
+        constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+        for (int i = 0; i < N / PER; ++i) {
+            const uint4 u = ld_stream_v4(p + i * PER);
+            const T *t = reinterpret_cast<const T *>(&u);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) v[i * PER + j] = to_f32<T>(t[j]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = to_f32<T>(p[i]);
+    }
+}
+template <class T, int N, bool VEC>
+__device__ __forceinline__ void store_row(T *p, const float (&v)[N]) {
+    if (VEC) {
+        constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+        for (int i = 0; i < N / PER; ++i) {
+            uint4 u;
+            T *t = reinterpret_cast<T *>(&u);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) t[j] = from_f32<T>(v[i * PER + j]);
+            reinterpret_cast<uint4 *>(p)[i] = u;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = from_f32<T>(v[i]);
+    }
+}
+
+// ------------------------------------------------------------------ quantise
+// A thread takes 8 inputs, four threads a block of 32.  Row r goes to row r of the output, or
+// to the rows inv_pos[r * k + j], j < k (entries outside [0, out_rows) are skipped).
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) mxfp4_quantize_kernel(const T *__restrict__ x, int64_t ld, int rows, int K,
+                                                             const int *__restrict__ inv_pos, int k, int out_rows,
+                                                             uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+    const int per_row = K / 8;
+    const int64_t total = (int64_t)rows * per_row;
+    // total is a multiple of four: the threads of a block of 32 inputs are all in or all out
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int r = (int)(i / per_row), g = (int)(i - (int64_t)r * per_row);
+        float v[8];
+        load_row<T, 8, VEC>(x + r * ld + g * 8, v);
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+        const unsigned team = 0xfu << (threadIdx.x & 28);
+        amax = max(amax, __shfl_xor_sync(team, amax, 1));
+        amax = max(amax, __shfl_xor_sync(team, amax, 2));
+        const uint32_t s = mx_scale_byte(amax);
+        uint32_t c = 0x77777777u;
+        if (s != 255u) {
+            const float inv = mx_inverse(s);
+            c = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c |= e2m1x2_code(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
+        }
+        if (!inv_pos) {
+            *reinterpret_cast<uint32_t *>(codes + (size_t)r * (K / 2) + g * 4) = c;
+            if ((g & 3) == 0) scales[(size_t)r * (K / MX_BLOCK) + (g >> 2)] = (uint8_t)s;
+        } else {
+            for (int j = 0; j < k; ++j) {
+                const int p = inv_pos[(size_t)r * k + j];
+                if (p < 0 || p >= out_rows) continue;
+                *reinterpret_cast<uint32_t *>(codes + (size_t)p * (K / 2) + g * 4) = c;
+                if ((g & 3) == 0) scales[(size_t)p * (K / MX_BLOCK) + (g >> 2)] = (uint8_t)s;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ dequantise
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) mxfp4_dequantize_kernel(const uint8_t *__restrict__ codes,
+                                                               const uint8_t *__restrict__ scales, int rows, int K,
+                                                               T *__restrict__ out, int64_t ld) {
+    const int per_row = K / 8;
+    const int64_t total = (int64_t)rows * per_row;
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int r = (int)(i / per_row), g = (int)(i - (int64_t)r * per_row);
+        const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(codes + (size_t)r * (K / 2)) + g);
+        const float s = e8m0_value(scales[(size_t)r * (K / MX_BLOCK) + (g >> 2)]);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(e2m1x2_value((c >> (8 * j)) & 0xFFu));
+            v[2 * j] = f.x * s;
+            v[2 * j + 1] = f.y * s;
+        }
+        store_row<T, 8, VEC>(out + r * ld + g * 8, v);
+    }
+}
+
+// ------------------------------------------------------------------ packed weights
+// An expert's matrix [N][K] is cut into tiles of 128 rows x 256 inputs (both filled up with
+// zeros), ordered (row tile, input tile), 17408 contiguous bytes each:
+//   bytes [0, 16384):     the codes as shared memory wants them: row r at r * 128, its 16-byte
+//                         chunk c (32 inputs) at chunk c ^ (r % 8)  (128-byte swizzle)
+//   bytes [16384, 17408): the scales, 512 bytes for each 128 inputs: four bytes (one per 32
+//                         inputs) of row r at (r % 32) * 16 + (r / 32) * 4
+// Gated matrices hold 2N rows: gate row i in row 2i, up row i in row 2i + 1.
+constexpr int MX_TM = 128, MX_TK = 256;
+constexpr int MX_CODE_BYTES = MX_TM * MX_TK / 2;
+constexpr int MX_TILE_BYTES = MX_CODE_BYTES + MX_TM * MX_TK / MX_BLOCK;   // 17408
+__host__ __device__ constexpr size_t mx_expert_bytes(int rows, int K) {
+    return (size_t)((rows + MX_TM - 1) / MX_TM) * ((K + MX_TK - 1) / MX_TK) * MX_TILE_BYTES;
+}
+__host__ __device__ constexpr uint32_t mx_code_off(int r, int chunk) { return (uint32_t)(r * 128 + ((chunk ^ (r & 7)) << 4)); }
+__host__ __device__ constexpr uint32_t mx_scale_off(int r, int blk) {
+    return (uint32_t)(MX_CODE_BYTES + (blk >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (blk & 3));
+}
+
+// One thread per (expert, packed row, block of 32 inputs), filler included.
+__global__ void __launch_bounds__(256) mxfp4_pack_kernel(const uint8_t *__restrict__ c0, const uint8_t *__restrict__ s0,
+                                                         const uint8_t *__restrict__ c1, const uint8_t *__restrict__ s1,
+                                                         int E, int N, int K, uint8_t *__restrict__ packed) {
+    const int mats = c1 ? 2 : 1, rows = N * mats;
+    const int row_tiles = (rows + MX_TM - 1) / MX_TM, k_tiles = (K + MX_TK - 1) / MX_TK;
+    const int64_t per_tile = MX_TM * (MX_TK / MX_BLOCK);
+    const int64_t total = (int64_t)E * row_tiles * k_tiles * per_tile;
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t tile = i / per_tile;
+        const int in = (int)(i - tile * per_tile), r = in >> 3, blk = in & 7;
+        const int kt = (int)(tile % k_tiles);
+        const int64_t rest = tile / k_tiles;
+        const int rt = (int)(rest % row_tiles), e = (int)(rest / row_tiles);
+        const int row = rt * MX_TM + r, kb = kt * (MX_TK / MX_BLOCK) + blk;
+        uint4 c = make_uint4(0, 0, 0, 0);
+        uint8_t s = 127;
+        if (row < rows && kb < K / MX_BLOCK) {
+            const uint8_t *cs = mats == 2 && (row & 1) ? c1 : c0, *ss = mats == 2 && (row & 1) ? s1 : s0;
+            const size_t src = ((size_t)e * N + (mats == 2 ? row >> 1 : row)) * (K / MX_BLOCK) + kb;
+            c = *reinterpret_cast<const uint4 *>(cs + src * 16);
+            s = ss[src];
+        }
+        uint8_t *t = packed + (size_t)tile * MX_TILE_BYTES;
+        *reinterpret_cast<uint4 *>(t + mx_code_off(r, blk)) = c;
+        t[mx_scale_off(r, blk)] = s;
+    }
+}
+
+}  // namespace ds4

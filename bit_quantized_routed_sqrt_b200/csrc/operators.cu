@@ -1,0 +1,336 @@
+// operators.cu -- host side of the operators beside the layer: routing from given logits,
+// MXFP4 rows and expert products, and the weighted combine (include/ds4moe.h).
+//
+// The stateless calls launch on the caller's current device and stream and keep nothing; the
+// ds4moe_mxfp4 handle holds the packed matrices of one projection of E experts on one device.
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <new>
+#include <string>
+
+#include "../../include/ds4moe.h"
+#include "combine.cuh"
+#include "mxfp4.cuh"
+#include "mxfp4_product.cuh"
+#include "scored_router.cuh"
+
+using namespace ds4;
+
+struct ds4moe_mxfp4 {
+    int device = 0;
+    ds4moe_mxfp4_config cfg{};
+    int num_sms = 148;
+    cudaStream_t last_stream = nullptr;
+    bool loaded = false;
+    std::string err;
+    uint8_t *packed = nullptr;
+    size_t expert_bytes = 0;
+    int *status = nullptr;
+};
+
+namespace {
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool injected(const char *what) {
+    const char *v = getenv("DS4MOE_FAULT");
+    return v && strcmp(v, what) == 0;
+}
+bool float_type(int t) { return t == DS4MOE_F32 || t == DS4MOE_BF16 || t == DS4MOE_F16; }
+size_t size_of(int t) { return t == DS4MOE_F32 ? 4 : 2; }
+ds4moe_status launched() { return cudaGetLastError() == cudaSuccess ? DS4MOE_OK : DS4MOE_ECUDA; }
+
+ds4moe_status fail(ds4moe_mxfp4 *h, ds4moe_status st, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    h->err = buf;
+    return st;
+}
+
+#define CK(h, call)                                                                                          \
+    do {                                                                                                     \
+        cudaError_t e_ = (call);                                                                             \
+        if (e_ != cudaSuccess)                                                                               \
+            return fail((h), e_ == cudaErrorMemoryAllocation ? DS4MOE_ENOMEM : DS4MOE_ECUDA, "%s: %s (%s:%d)", \
+                        #call, cudaGetErrorString(e_), __FILE__, __LINE__);                                  \
+    } while (0)
+
+// The handle's device for the length of a call; the caller's current device again after it.
+struct OnDevice {
+    int before = -1;
+    cudaError_t err;
+    explicit OnDevice(int device) {
+        err = cudaGetDevice(&before);
+        if (err == cudaSuccess && before != device) err = cudaSetDevice(device);
+        else if (err == cudaSuccess) before = -1;
+    }
+    ~OnDevice() {
+        if (before >= 0) cudaSetDevice(before);
+    }
+};
+
+int blocks_for(int64_t threads) { return (int)std::min<int64_t>((threads + 255) / 256, 148 * 64); }
+
+// ------------------------------------------------------------------ routing from logits
+bool router_ok(const ds4moe_router *r) {
+    return r && r->n_experts >= 1 && r->n_experts <= SR_MAX_EXPERTS && r->top_k >= 1 && r->top_k <= SR_MAX_TOPK &&
+           r->score >= DS4MOE_SCORE_SOFTMAX && r->score <= DS4MOE_SCORE_SQRT_SOFTPLUS && r->n_groups >= 1 &&
+           r->n_groups <= SR_MAX_GROUPS && r->n_experts % r->n_groups == 0 && r->topk_groups >= 1 &&
+           r->topk_groups <= r->n_groups && r->top_k <= r->n_experts / r->n_groups * r->topk_groups &&
+           r->group_score >= DS4MOE_GROUP_MAX && r->group_score <= DS4MOE_GROUP_TOP2 &&
+           (r->renormalise == 0 || r->renormalise == 1) && r->scale - r->scale == 0.0f;
+}
+// Tokens a block: 64, or 256 once the counts of 64-token blocks would be a long column to add up.
+int route_block(int T) { return T <= 16384 ? 64 : 256; }
+size_t route_workspace(const ds4moe_router *r, int T) {
+    const int TB = route_block(T);
+    const size_t NB = ((size_t)T + TB - 1) / TB;
+    return NB <= 1 ? 0 : NB * r->n_experts * (4 + TB / 8);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ds4moe_route_logits_workspace(const ds4moe_router *r, int32_t T) {
+    return router_ok(r) && T > 0 ? route_workspace(r, T) : 0;
+}
+
+ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev, int32_t logits_type, int64_t ld,
+                                  int32_t T, const float *bias_dev, int32_t *topk_idx_dev, float *topk_w_dev,
+                                  int32_t *expert_offsets_dev, int32_t *sorted_token_dev, int32_t *sorted_slot_dev,
+                                  int32_t *inv_pos_dev, void *workspace_dev, size_t workspace_bytes, void *cuda_stream) {
+    if (!router_ok(r) || T < 0 || !float_type(logits_type) || ld < r->n_experts) return DS4MOE_EINVAL;
+    if ((int64_t)T * r->top_k > INT32_MAX) return DS4MOE_EINVAL;
+    if (injected("launch")) return DS4MOE_ECUDA;
+    const bool permute = expert_offsets_dev || sorted_token_dev || sorted_slot_dev || inv_pos_dev;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    if (T == 0) {
+        // no pair: the offsets are all zero
+        if (expert_offsets_dev &&
+            cudaMemsetAsync(expert_offsets_dev, 0, (r->n_experts + 1) * sizeof(int32_t), st) != cudaSuccess)
+            return DS4MOE_ECUDA;
+        return DS4MOE_OK;
+    }
+    if (!logits_dev || (uintptr_t)logits_dev % size_of(logits_type) || !topk_idx_dev || !topk_w_dev) return DS4MOE_EINVAL;
+    ScoredArgs a{};
+    a.E = r->n_experts; a.k = r->top_k; a.score = r->score; a.G = r->n_groups; a.topk_groups = r->topk_groups;
+    a.top2 = r->group_score == DS4MOE_GROUP_TOP2; a.renormalise = r->renormalise; a.scale = r->scale;
+    a.logits = logits_dev; a.type = logits_type; a.ld = ld;
+    a.T = T; a.TB = route_block(T); a.NB = (int)(((int64_t)T + a.TB - 1) / a.TB);
+    a.bias = bias_dev;
+    a.topk_idx = topk_idx_dev; a.topk_w = topk_w_dev;
+    a.offsets = expert_offsets_dev; a.sorted_token = sorted_token_dev; a.sorted_slot = sorted_slot_dev; a.inv_pos = inv_pos_dev;
+    if (permute && a.NB > 1) {
+        if (!workspace_dev || (uintptr_t)workspace_dev % 4 || workspace_bytes < route_workspace(r, T)) return DS4MOE_EINVAL;
+        a.cnt = static_cast<int *>(workspace_dev);
+        a.mask = reinterpret_cast<uint32_t *>(a.cnt + (size_t)a.NB * a.E);
+    }
+    const size_t smem = (a.G > 1 ? (size_t)SR_WARPS * a.E * 8 : 0) + (size_t)a.E * (a.TB / 8 + 4);
+    static_assert(SR_WARPS * SR_MAX_EXPERTS * 8 + SR_MAX_EXPERTS * (256 / 8 + 4) <= 227 * 1024, "shared memory per CTA");
+    auto launch = [&](auto kernel) {
+        if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        kernel<<<a.NB, 32 * SR_WARPS, smem, st>>>(a);
+    };
+    if (a.E <= 32) launch(scored_topk_kernel<1>);
+    else if (a.E <= 64) launch(scored_topk_kernel<2>);
+    else if (a.E <= 128) launch(scored_topk_kernel<4>);
+    else if (a.E <= 256) launch(scored_topk_kernel<8>);
+    else launch(scored_topk_kernel<16>);
+    ds4moe_status s = launched();
+    if (s != DS4MOE_OK || !permute || a.NB == 1) return s;
+    scored_permute_kernel<<<a.NB, 32 * SR_WARPS, (size_t)a.E * 8, st>>>(a);
+    return launched();
+}
+
+ds4moe_status ds4moe_mxfp4_quantize(const void *x_dev, int32_t x_type, int64_t ld, int32_t rows, int32_t K,
+                                    const int32_t *inv_pos_dev, int32_t top_k, int32_t out_rows, uint8_t *codes_dev,
+                                    uint8_t *scales_dev, void *cuda_stream) {
+    if (rows < 0 || out_rows < 0 || K <= 0 || K % MX_BLOCK || !float_type(x_type) || ld < K) return DS4MOE_EINVAL;
+    if (inv_pos_dev ? top_k < 1 || top_k > SR_MAX_TOPK : out_rows < rows) return DS4MOE_EINVAL;
+    if (injected("launch")) return DS4MOE_ECUDA;
+    if (rows == 0 || out_rows == 0) return DS4MOE_OK;
+    if (!x_dev || (uintptr_t)x_dev % size_of(x_type) || !codes_dev || !aligned16(codes_dev) || !scales_dev) return DS4MOE_EINVAL;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    const bool vec = aligned16(x_dev) && ld * size_of(x_type) % 16 == 0;
+    const int grid = blocks_for((int64_t)rows * (K / 8));
+    auto go = [&](auto kernel, auto *x) {
+        kernel<<<grid, 256, 0, st>>>(x, ld, rows, K, inv_pos_dev, top_k, out_rows, codes_dev, scales_dev);
+    };
+    if (x_type == DS4MOE_F32) {
+        auto *x = static_cast<const float *>(x_dev);
+        if (vec) go(mxfp4_quantize_kernel<float, true>, x); else go(mxfp4_quantize_kernel<float, false>, x);
+    } else if (x_type == DS4MOE_BF16) {
+        auto *x = static_cast<const __nv_bfloat16 *>(x_dev);
+        if (vec) go(mxfp4_quantize_kernel<__nv_bfloat16, true>, x); else go(mxfp4_quantize_kernel<__nv_bfloat16, false>, x);
+    } else {
+        auto *x = static_cast<const __half *>(x_dev);
+        if (vec) go(mxfp4_quantize_kernel<__half, true>, x); else go(mxfp4_quantize_kernel<__half, false>, x);
+    }
+    return launched();
+}
+
+ds4moe_status ds4moe_mxfp4_dequantize(const uint8_t *codes_dev, const uint8_t *scales_dev, int32_t rows, int32_t K,
+                                      void *out_dev, int32_t out_type, int64_t ld, void *cuda_stream) {
+    if (rows < 0 || K <= 0 || K % MX_BLOCK || !float_type(out_type) || ld < K) return DS4MOE_EINVAL;
+    if (injected("launch")) return DS4MOE_ECUDA;
+    if (rows == 0) return DS4MOE_OK;
+    if (!codes_dev || !aligned16(codes_dev) || !scales_dev || !out_dev || (uintptr_t)out_dev % size_of(out_type)) return DS4MOE_EINVAL;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    const bool vec = aligned16(out_dev) && ld * size_of(out_type) % 16 == 0;
+    const int grid = blocks_for((int64_t)rows * (K / 8));
+    auto go = [&](auto kernel, auto *out) { kernel<<<grid, 256, 0, st>>>(codes_dev, scales_dev, rows, K, out, ld); };
+    if (out_type == DS4MOE_F32) {
+        auto *o = static_cast<float *>(out_dev);
+        if (vec) go(mxfp4_dequantize_kernel<float, true>, o); else go(mxfp4_dequantize_kernel<float, false>, o);
+    } else if (out_type == DS4MOE_BF16) {
+        auto *o = static_cast<__nv_bfloat16 *>(out_dev);
+        if (vec) go(mxfp4_dequantize_kernel<__nv_bfloat16, true>, o); else go(mxfp4_dequantize_kernel<__nv_bfloat16, false>, o);
+    } else {
+        auto *o = static_cast<__half *>(out_dev);
+        if (vec) go(mxfp4_dequantize_kernel<__half, true>, o); else go(mxfp4_dequantize_kernel<__half, false>, o);
+    }
+    return launched();
+}
+
+ds4moe_status ds4moe_combine(const void *o_dev, int32_t o_type, int64_t o_rows, int32_t T, int32_t top_k, int32_t H,
+                             const int32_t *inv_pos_dev, const float *topk_w_dev, const void *add_dev, int32_t add_type,
+                             void *y_dev, int32_t y_type, void *cuda_stream) {
+    if (T < 0 || H <= 0 || top_k < 1 || top_k > SR_MAX_TOPK || o_rows < 0 || !float_type(o_type) || !float_type(y_type) ||
+        (add_dev && !float_type(add_type)))
+        return DS4MOE_EINVAL;
+    if (injected("launch")) return DS4MOE_ECUDA;
+    if (T == 0) return DS4MOE_OK;
+    if ((o_rows > 0 && !o_dev) || !inv_pos_dev || !topk_w_dev || !y_dev) return DS4MOE_EINVAL;
+    if ((uintptr_t)o_dev % size_of(o_type) || (uintptr_t)y_dev % size_of(y_type) ||
+        (add_dev && (uintptr_t)add_dev % size_of(add_type)))
+        return DS4MOE_EINVAL;
+    CombineArgs a{o_dev, o_rows, T, top_k, H, inv_pos_dev, topk_w_dev, add_dev, add_type, y_dev};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    const int grid = blocks_for((int64_t)T * H);
+    auto go = [&](auto kernel) { kernel<<<grid, 256, 0, st>>>(a); };
+    auto with = [&](auto o) {
+        using TO = decltype(o);
+        if (y_type == DS4MOE_F32) go(combine_kernel<TO, float>);
+        else if (y_type == DS4MOE_BF16) go(combine_kernel<TO, __nv_bfloat16>);
+        else go(combine_kernel<TO, __half>);
+    };
+    if (o_type == DS4MOE_F32) with(float{});
+    else if (o_type == DS4MOE_BF16) with(__nv_bfloat16{});
+    else with(__half{});
+    return launched();
+}
+
+const char *ds4moe_mxfp4_last_error(const ds4moe_mxfp4 *h) { return h ? h->err.c_str() : "null handle"; }
+
+ds4moe_status ds4moe_mxfp4_create(const ds4moe_mxfp4_config *cfg, int cuda_device, ds4moe_mxfp4 **out) {
+    if (!cfg || !out) return DS4MOE_EINVAL;
+    *out = nullptr;
+    if (cfg->n_experts < 1 || cfg->n_experts > SR_MAX_EXPERTS || cfg->n_out < 1 || cfg->n_out > 65536 || cfg->n_in < MX_BLOCK ||
+        cfg->n_in > 65536 || cfg->n_in % MX_BLOCK || (cfg->gated != 0 && cfg->gated != 1))
+        return DS4MOE_EINVAL;
+    if (injected("alloc")) return DS4MOE_ENOMEM;
+    ds4moe_mxfp4 *h = new (std::nothrow) ds4moe_mxfp4();
+    if (!h) return DS4MOE_ENOMEM;
+    h->cfg = *cfg;
+    h->device = cuda_device;
+    h->expert_bytes = mx_expert_bytes(cfg->n_out * (cfg->gated ? 2 : 1), cfg->n_in);
+    OnDevice on(cuda_device);
+    cudaError_t e = on.err;
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, cuda_device);
+    if (e == cudaSuccess) e = cudaMalloc(&h->packed, h->expert_bytes * cfg->n_experts);
+    if (e == cudaSuccess) e = cudaMalloc(&h->status, 256);
+    if (e == cudaSuccess) e = cudaMemset(h->status, 0, 256);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        if (h->packed) cudaFree(h->packed);
+        if (h->status) cudaFree(h->status);
+        delete h;
+        return e == cudaErrorMemoryAllocation ? DS4MOE_ENOMEM : DS4MOE_ECUDA;
+    }
+    *out = h;
+    return DS4MOE_OK;
+}
+
+void ds4moe_mxfp4_destroy(ds4moe_mxfp4 *h) {
+    if (!h) return;
+    OnDevice on(h->device);
+    cudaDeviceSynchronize();
+    cudaFree(h->packed);
+    cudaFree(h->status);
+    delete h;
+}
+
+ds4moe_status ds4moe_mxfp4_load(ds4moe_mxfp4 *h, const uint8_t *codes_dev, const uint8_t *scales_dev,
+                                const uint8_t *up_codes_dev, const uint8_t *up_scales_dev, void *cuda_stream) {
+    if (!h) return DS4MOE_EINVAL;
+    const ds4moe_mxfp4_config &g = h->cfg;
+    if (!codes_dev || !scales_dev || (g.gated && (!up_codes_dev || !up_scales_dev)))
+        return fail(h, DS4MOE_EINVAL, "null weight pointer");
+    if (!g.gated && (up_codes_dev || up_scales_dev)) return fail(h, DS4MOE_EINVAL, "a second matrix for a handle that is not gated");
+    if (!aligned16(codes_dev) || (g.gated && !aligned16(up_codes_dev))) return fail(h, DS4MOE_EINVAL, "codes must be 16-byte aligned");
+    if (injected("h2d")) return fail(h, DS4MOE_ECUDA, "weight packing failed (injected: DS4MOE_FAULT=h2d)");
+    OnDevice on(h->device);
+    CK(h, on.err);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    const int64_t n = (int64_t)g.n_experts * (h->expert_bytes / MX_TILE_BYTES) * MX_TM * (MX_TK / MX_BLOCK);
+    mxfp4_pack_kernel<<<blocks_for(n), 256, 0, st>>>(codes_dev, scales_dev, g.gated ? up_codes_dev : nullptr,
+                                                    g.gated ? up_scales_dev : nullptr, g.n_experts, g.n_out, g.n_in, h->packed);
+    CK(h, cudaGetLastError());
+    h->loaded = true;
+    h->last_stream = st;
+    return DS4MOE_OK;
+}
+
+ds4moe_status ds4moe_mxfp4_product(ds4moe_mxfp4 *h, const uint8_t *a_codes_dev, const uint8_t *a_scales_dev, int32_t rows,
+                                   const int32_t *expert_offsets_dev, void *out_dev, int32_t out_type, int64_t ld,
+                                   uint8_t *out_scales_dev, void *cuda_stream) {
+    if (!h) return DS4MOE_EINVAL;
+    const ds4moe_mxfp4_config &g = h->cfg;
+    if (injected("launch")) return fail(h, DS4MOE_ECUDA, "kernel launch failed (injected: DS4MOE_FAULT=launch)");
+    if (!h->loaded) return fail(h, DS4MOE_ESTATE, "no weights loaded");
+    if (rows < 0) return fail(h, DS4MOE_EINVAL, "rows=%d is negative", rows);
+    if (!float_type(out_type) && out_type != DS4MOE_MXFP4) return fail(h, DS4MOE_EINVAL, "unknown output type %d", out_type);
+    if (out_type == DS4MOE_MXFP4 ? g.n_out % MX_BLOCK != 0 || ld != g.n_out || !out_scales_dev : out_scales_dev != nullptr)
+        return fail(h, DS4MOE_EINVAL, "an MXFP4 output needs n_out %% 32 == 0, ld == n_out and scales; the others take no scales");
+    if (ld < g.n_out) return fail(h, DS4MOE_EINVAL, "ld is below n_out");
+    if (!expert_offsets_dev && g.n_experts != 1) return fail(h, DS4MOE_EINVAL, "expert offsets are required");
+    if (rows == 0) return DS4MOE_OK;
+    if (!a_codes_dev || !a_scales_dev || !out_dev) return fail(h, DS4MOE_EINVAL, "null buffer");
+    if (!aligned16(a_codes_dev) || !aligned16(out_dev)) return fail(h, DS4MOE_EINVAL, "codes and output must be 16-byte aligned");
+    OnDevice on(h->device);
+    CK(h, on.err);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+    h->last_stream = st;
+    MxArgs a{};
+    a.w = h->packed; a.expert_bytes = h->expert_bytes;
+    a.E = g.n_experts; a.N = g.n_out; a.K = g.n_in; a.gated = g.gated;
+    a.a_codes = a_codes_dev; a.a_scales = a_scales_dev; a.rows = rows; a.offsets = expert_offsets_dev;
+    a.out = out_dev; a.out_scales = out_scales_dev; a.out_type = out_type; a.ld = ld;
+    a.status = h->status;
+    const int64_t warps = (int64_t)rows * ((g.n_out + 31) / 32);
+    mxfp4_product_simple_kernel<<<blocks_for(warps * 32), 256, 0, st>>>(a);
+    CK(h, cudaGetLastError());
+    return DS4MOE_OK;
+}
+
+ds4moe_status ds4moe_mxfp4_sync_status(ds4moe_mxfp4 *h) {
+    if (!h) return DS4MOE_EINVAL;
+    OnDevice on(h->device);
+    CK(h, on.err);
+    CK(h, cudaStreamSynchronize(h->last_stream));
+    int st = 0;
+    CK(h, cudaMemcpy(&st, h->status, 4, cudaMemcpyDeviceToHost));
+    if (st != 0) {
+        CK(h, cudaMemset(h->status, 0, 4));
+        return fail(h, (ds4moe_status)st, "device status %d", st);
+    }
+    return DS4MOE_OK;
+}
+
+}  // extern "C"

@@ -233,6 +233,138 @@ ds4moe_status ds4moe_get_stats(ds4moe *h, ds4moe_stats *out);
 ds4moe_status ds4moe_get_trace(ds4moe *h, int64_t *out, int32_t max_records, int32_t *n_records,
                                int32_t *unit_bounds);
 
+/* ======================================================================================
+ * Operators beside the layer: routing from given logits, MXFP4 rows and expert products,
+ * and the weighted combine.  Together they run an MoE FFN whose router differs from the
+ * layer's own and whose experts are held in MXFP4 (4-bit floats with one scale per 32):
+ *     route_logits -> mxfp4_quantize (into expert order) -> mxfp4_product (gate/up, gated,
+ *     MXFP4 out) -> mxfp4_product (down) -> combine (with the shared expert's rows).
+ * Calls without a handle launch on the calling thread's current device, which must be that
+ * of the buffers and the stream; they keep nothing and may run concurrently on different
+ * outputs and workspaces.  They return DS4MOE_EINVAL for an argument out of range, NULL or
+ * misaligned.  Every call here only enqueues work (none allocates), so it can be captured
+ * into a CUDA graph.  The library has no training path: none of these has a backward pass.
+ * Element types: */
+typedef enum {
+    DS4MOE_F32 = 0,
+    DS4MOE_BF16 = 1,
+    DS4MOE_F16 = 2,
+    DS4MOE_MXFP4 = 3 /* E2M1 codes, two to a byte (even element in the low nibble), with an
+                        E8M0 scale byte per 32 elements of a row: value * 2^(scale - 127) */
+} ds4moe_dtype;
+
+typedef enum { DS4MOE_SCORE_SOFTMAX = 0, DS4MOE_SCORE_SIGMOID = 1, DS4MOE_SCORE_SQRT_SOFTPLUS = 2 } ds4moe_score;
+typedef enum { DS4MOE_GROUP_MAX = 0, DS4MOE_GROUP_TOP2 = 1 } ds4moe_group_score;
+
+/* How experts are chosen and weighted (ds4moe_route_logits). */
+typedef struct {
+    int32_t n_experts;   /* E: 1 .. 512 */
+    int32_t top_k;       /* k: 1 .. 32, at most topk_groups * E / n_groups */
+    int32_t score;       /* DS4MOE_SCORE_*: s = softmax(l), sigmoid(l) or sqrt(softplus(l)) */
+    int32_t n_groups;    /* 1 .. 32, divides E: group g holds experts g E/n_groups .. */
+    int32_t topk_groups; /* 1 .. n_groups: groups that a token may choose from */
+    int32_t group_score; /* DS4MOE_GROUP_MAX: the best choice value of a group;
+                            DS4MOE_GROUP_TOP2: the sum of its two best (of one, where it has one) */
+    int32_t renormalise; /* 1: the k weights are divided by their sum */
+    float scale;         /* factor on the weights (finite) */
+} ds4moe_router;
+
+/* Bytes of workspace for T tokens (0 for up to 64 tokens, and for an invalid router). */
+size_t ds4moe_route_logits_workspace(const ds4moe_router *r, int32_t T);
+
+/* Routing of T tokens from their router logits [T][ld] (F32, BF16 or F16, ld >= E elements
+ * between rows).
+ *  Choice: an expert's choice value is s + bias (bias_dev [E] fp32: for the choice alone,
+ *  the weight is that of s).  The topk_groups best groups, then the k experts of those
+ *  groups with the largest choice values, in descending order; ties go to the lower index.
+ *  Choice values are compared as fp64 evaluations of them; without a bias experts are
+ *  compared by their logits, which order as their scores do.
+ *  Weights: w_j = scale * s_j, or scale * s_j / sum_i s_i; the quotient is that of the exact
+ *  scores, also where they underflow.
+ *  A logit of -inf or NaN (or a bias that makes the choice value so) leaves its expert out;
+ *  +inf counts as the largest finite fp32 value.  Where fewer than k experts are left, the
+ *  remaining slots get index -1 and weight 0 and take no place in the permutation.
+ *  Outputs: topk_idx_dev, topk_w_dev [T][k]; the permutation as in ds4moe_route, each of its
+ *  four pointers may be NULL.  expert_offsets_dev [E+1] counts placed pairs only; entries of
+ *  sorted_token_dev / sorted_slot_dev [T*k] from expert_offsets_dev[E] on are left as they
+ *  were; inv_pos_dev [T*k] is -1 for a slot without an expert.  T = 0 zeroes the offsets.
+ *  workspace_dev: at least ds4moe_route_logits_workspace bytes, 4-byte aligned, needed when
+ *  that is not 0 and a permutation output is given; its contents do not matter.  Two calls
+ *  (or captured graphs) that may run at the same time need a workspace each. */
+ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev, int32_t logits_type, int64_t ld,
+                                  int32_t T, const float *bias_dev, int32_t *topk_idx_dev, float *topk_w_dev,
+                                  int32_t *expert_offsets_dev, int32_t *sorted_token_dev, int32_t *sorted_slot_dev,
+                                  int32_t *inv_pos_dev, void *workspace_dev, size_t workspace_bytes, void *cuda_stream);
+
+/* MXFP4 quantisation of rows x [rows][ld] (F32, BF16 or F16; K elements each, K a multiple
+ * of 32).  A block of 32 gets the scale 2^e, e = max(floor(log2(max |x|)) - 2, -127), and the
+ * codes of x / 2^e rounded to the nearest E2M1 value (ties to even), saturated at +-6.  A
+ * block with a NaN or an infinity gets scale byte 255 (NaN).
+ *  inv_pos_dev NULL: row r -> row r (out_rows >= rows).  Otherwise inv_pos_dev [rows][top_k]
+ *  and row r -> rows inv_pos[r][j], j < top_k (1 .. 32); entries outside [0, out_rows) are
+ *  skipped, so the rows of tokens land in expert order.  Rows that are no target are left as
+ *  they were.  codes_dev [out_rows][K/2] (16-byte aligned), scales_dev [out_rows][K/32]. */
+ds4moe_status ds4moe_mxfp4_quantize(const void *x_dev, int32_t x_type, int64_t ld, int32_t rows, int32_t K,
+                                    const int32_t *inv_pos_dev, int32_t top_k, int32_t out_rows, uint8_t *codes_dev,
+                                    uint8_t *scales_dev, void *cuda_stream);
+
+/* The values of MXFP4 rows: codes_dev [rows][K/2] (16-byte aligned), scales_dev [rows][K/32]
+ * -> out_dev [rows][ld] of out_type (F32, BF16 or F16; rounded to nearest even where the type
+ * does not hold the value). */
+ds4moe_status ds4moe_mxfp4_dequantize(const uint8_t *codes_dev, const uint8_t *scales_dev, int32_t rows, int32_t K,
+                                      void *out_dev, int32_t out_type, int64_t ld, void *cuda_stream);
+
+/* One projection of E experts in MXFP4 on one device (opaque, library-owned).  Like a layer
+ * handle it is not thread-safe. */
+typedef struct ds4moe_mxfp4 ds4moe_mxfp4;
+typedef struct {
+    int32_t n_experts; /* E: 1 .. 512 */
+    int32_t n_out;     /* N, outputs: 1 .. 65536 */
+    int32_t n_in;      /* K, inputs: a multiple of 32, 32 .. 65536 */
+    int32_t gated;     /* 1: two matrices, and the output is silu(gate x) * (up x) */
+} ds4moe_mxfp4_config;
+
+/* Create a handle on CUDA device `cuda_device` and allocate its weights.  *out is set only on
+ * DS4MOE_OK.  The calling thread's current device is the same after this call and after the
+ * other ds4moe_mxfp4_* calls.  DS4MOE_FAULT=alloc applies. */
+ds4moe_status ds4moe_mxfp4_create(const ds4moe_mxfp4_config *cfg, int cuda_device, ds4moe_mxfp4 **out);
+/* Wait for the device and free the handle; NULL is ignored. */
+void ds4moe_mxfp4_destroy(ds4moe_mxfp4 *h);
+
+/* Lay out the weights for the product, from device memory: codes_dev [E][N][K/2] (16-byte
+ * aligned), scales_dev [E][N][K/32]; a gated handle takes the gate's and the up projection's
+ * (both NULL otherwise).  Only enqueues; the sources may be freed once the stream has passed
+ * it.  May be called again to replace the weights.  DS4MOE_FAULT=h2d applies. */
+ds4moe_status ds4moe_mxfp4_load(ds4moe_mxfp4 *h, const uint8_t *codes_dev, const uint8_t *scales_dev,
+                                const uint8_t *up_codes_dev, const uint8_t *up_scales_dev, void *cuda_stream);
+
+/* Products of rows with their experts' matrices: rows expert_offsets_dev[e] ..
+ * expert_offsets_dev[e+1] - 1 of a (a_codes_dev [rows][K/2], 16-byte aligned; a_scales_dev
+ * [rows][K/32]) belong to expert e; NULL offsets give every row to the one expert of a handle
+ * with n_experts = 1.  out[r][n] = sum_k a[r][k] W[n][k], or silu(gate) * up, computed with
+ * fp32 sums and rounded once to out_type.  out_dev is [rows][ld] (16-byte aligned); MXFP4
+ * output (N % 32 == 0, ld == N) is quantised as by ds4moe_mxfp4_quantize into out_dev
+ * [rows][N/2] and out_scales_dev [rows][N/32] (NULL for the other types).  Rows behind
+ * expert_offsets_dev[E] are neither used nor written.  Products whose magnitude is below the
+ * normal range of fp32 may count as zero. */
+ds4moe_status ds4moe_mxfp4_product(ds4moe_mxfp4 *h, const uint8_t *a_codes_dev, const uint8_t *a_scales_dev, int32_t rows,
+                                   const int32_t *expert_offsets_dev, void *out_dev, int32_t out_type, int64_t ld,
+                                   uint8_t *out_scales_dev, void *cuda_stream);
+
+/* Synchronise the last stream the handle used and return its sticky device status; clears it. */
+ds4moe_status ds4moe_mxfp4_sync_status(ds4moe_mxfp4 *h);
+/* One-line detail of the handle's last error, owned by the handle ("" if none). */
+const char *ds4moe_mxfp4_last_error(const ds4moe_mxfp4 *h);
+
+/* The experts' rows back in token order: y[t] = add[t] + sum_j w[t][j] o[inv_pos[t][j]], the
+ * slots in order, in fp32, rounded once to y_type.  o_dev [o_rows][H], inv_pos_dev and
+ * topk_w_dev [T][top_k]; a slot whose row is outside [0, o_rows) adds nothing, whatever its
+ * weight.  add_dev [T][H] (the shared expert's rows) may be NULL, and may be y_dev itself
+ * where the types are the same. */
+ds4moe_status ds4moe_combine(const void *o_dev, int32_t o_type, int64_t o_rows, int32_t T, int32_t top_k, int32_t H,
+                             const int32_t *inv_pos_dev, const float *topk_w_dev, const void *add_dev, int32_t add_type,
+                             void *y_dev, int32_t y_type, void *cuda_stream);
+
 /* Static text for a status code. */
 const char *ds4moe_status_string(ds4moe_status s);
 
