@@ -3,6 +3,8 @@
 //
 // The stateless calls launch on the caller's current device and stream and keep nothing; the
 // ds4moe_mxfp4 handle holds the packed matrices of one projection of E experts on one device.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
@@ -91,6 +93,45 @@ size_t route_workspace(const ds4moe_router *r, int T) {
     const int TB = route_block(T);
     const size_t NB = ((size_t)T + TB - 1) / TB;
     return NB <= 1 ? 0 : NB * r->n_experts * (4 + TB / 8);
+}
+
+// ------------------------------------------------------------------ MXFP4 products
+// Tensor map of the rows' codes, [rows][K / 2] bytes, with boxes of 128 bytes (one K step) x
+// box_rows and the 128-byte swizzle.
+bool row_map(CUtensorMap *m, const void *codes, int rows, int K, int box_rows) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)K / 2};
+    cuuint32_t box[2] = {MX_TK / 2, (cuuint32_t)box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C>
+ds4moe_status run_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
+    CUtensorMap tm{};
+    if (!row_map(&tm, a.a_codes, a.rows, a.K, C::BOX)) return fail(h, DS4MOE_ECUDA, "tensor map of the rows");
+    CK(h, cudaFuncSetAttribute(mxfp4_product_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM));
+    mxfp4_product_kernel<C><<<h->num_sms, MX_THREADS, C::SMEM, st>>>(tm, a);
+    CK(h, cudaGetLastError());
+    return DS4MOE_OK;
+}
+template <bool GATED>
+ds4moe_status pick_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
+    const double per_expert = (double)a.rows / std::min(a.rows, a.E);
+    if (per_expert <= 24) return run_product<MxCfg<32, 8, 8, GATED>>(h, a, st);
+    if (per_expert <= 112) return run_product<MxCfg<128, 32, 5, GATED>>(h, a, st);
+    return run_product<MxCfg<192, 32, 4, GATED>>(h, a, st);
 }
 
 }  // namespace
@@ -302,7 +343,9 @@ ds4moe_status ds4moe_mxfp4_product(ds4moe_mxfp4 *h, const uint8_t *a_codes_dev, 
     if (!expert_offsets_dev && g.n_experts != 1) return fail(h, DS4MOE_EINVAL, "expert offsets are required");
     if (rows == 0) return DS4MOE_OK;
     if (!a_codes_dev || !a_scales_dev || !out_dev) return fail(h, DS4MOE_EINVAL, "null buffer");
-    if (!aligned16(a_codes_dev) || !aligned16(out_dev)) return fail(h, DS4MOE_EINVAL, "codes and output must be 16-byte aligned");
+    if (!aligned16(a_codes_dev)) return fail(h, DS4MOE_EINVAL, "codes must be 16-byte aligned");
+    if ((uintptr_t)out_dev % (out_type == DS4MOE_MXFP4 ? 16 : size_of(out_type)))
+        return fail(h, DS4MOE_EINVAL, "the output is not aligned to its elements (MXFP4: to 16 bytes)");
     OnDevice on(h->device);
     CK(h, on.err);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
@@ -313,10 +356,8 @@ ds4moe_status ds4moe_mxfp4_product(ds4moe_mxfp4 *h, const uint8_t *a_codes_dev, 
     a.a_codes = a_codes_dev; a.a_scales = a_scales_dev; a.rows = rows; a.offsets = expert_offsets_dev;
     a.out = out_dev; a.out_scales = out_scales_dev; a.out_type = out_type; a.ld = ld;
     a.status = h->status;
-    const int64_t warps = (int64_t)rows * ((g.n_out + 31) / 32);
-    mxfp4_product_simple_kernel<<<blocks_for(warps * 32), 256, 0, st>>>(a);
-    CK(h, cudaGetLastError());
-    return DS4MOE_OK;
+    a.vec_out = out_type != DS4MOE_MXFP4 && aligned16(out_dev) && ld * size_of(out_type) % 16 == 0;
+    return g.gated ? pick_product<true>(h, a, st) : pick_product<false>(h, a, st);
 }
 
 ds4moe_status ds4moe_mxfp4_sync_status(ds4moe_mxfp4 *h) {

@@ -2,13 +2,13 @@
 // bias on the choice, groups, top-k, renormalised weights, and the token -> expert permutation.
 #pragma once
 #include "combine.cuh"
+#include "scan.cuh"
 
 namespace ds4 {
 
-constexpr int SR_MAX_EXPERTS = 512;
 constexpr int SR_MAX_TOPK = 32;
 constexpr int SR_MAX_GROUPS = 32;
-constexpr int SR_WARPS = 8;
+constexpr int SR_WARPS = SCAN_THREADS / 32;
 
 enum : int { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1, SCORE_SQRT_SOFTPLUS = 2 };
 
@@ -176,30 +176,6 @@ __device__ __forceinline__ void scored_scatter(const ScoredArgs &p, int t0, int 
         }
         if (p.inv_pos) p.inv_pos[pair] = pos;
     }
-}
-
-// Exclusive scan of v[0..E) in place by the block (E <= 512, 256 threads); total to every thread.
-__device__ __forceinline__ int block_scan(int *v, int E, int *part) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int a = 2 * tid < E ? v[2 * tid] : 0, b = 2 * tid + 1 < E ? v[2 * tid + 1] : 0;
-    int s = a + b;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += u;
-    }
-    if (lane == 31) part[warp] = s;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < SR_WARPS; ++w) {
-        if (w < warp) before += part[w];
-        total += part[w];
-    }
-    const int ex = before + s - a - b;
-    if (2 * tid < E) v[2 * tid] = ex;
-    if (2 * tid + 1 < E) v[2 * tid + 1] = ex + a;
-    __syncthreads();
-    return total;
 }
 
 // Top-k of TB tokens a block.  With one block the permutation follows at once; otherwise the

@@ -342,9 +342,9 @@ ds4moe_status ds4moe_mxfp4_load(ds4moe_mxfp4 *h, const uint8_t *codes_dev, const
  * expert_offsets_dev[e+1] - 1 of a (a_codes_dev [rows][K/2], 16-byte aligned; a_scales_dev
  * [rows][K/32]) belong to expert e; NULL offsets give every row to the one expert of a handle
  * with n_experts = 1.  out[r][n] = sum_k a[r][k] W[n][k], or silu(gate) * up, computed with
- * fp32 sums and rounded once to out_type.  out_dev is [rows][ld] (16-byte aligned); MXFP4
- * output (N % 32 == 0, ld == N) is quantised as by ds4moe_mxfp4_quantize into out_dev
- * [rows][N/2] and out_scales_dev [rows][N/32] (NULL for the other types).  Rows behind
+ * fp32 sums and rounded once to out_type.  out_dev is [rows][ld], ld >= N; MXFP4 output
+ * (N % 32 == 0, ld == N) is quantised as by ds4moe_mxfp4_quantize into out_dev [rows][N/2]
+ * (16-byte aligned) and out_scales_dev [rows][N/32] (NULL for the other types).  Rows behind
  * expert_offsets_dev[E] are neither used nor written.  Products whose magnitude is below the
  * normal range of fp32 may count as zero. */
 ds4moe_status ds4moe_mxfp4_product(ds4moe_mxfp4 *h, const uint8_t *a_codes_dev, const uint8_t *a_scales_dev, int32_t rows,
