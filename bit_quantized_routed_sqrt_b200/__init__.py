@@ -237,35 +237,40 @@ def _flat(t, dtype: str, n: int, what: str, device):
 
 
 _dtypes = {}
+_raw_stream = None
 
 
 def _torch_dtypes():
+    global _raw_stream
     if not _dtypes:
         import torch
         _dtypes.update(int32=torch.int32, uint8=torch.uint8, float32=torch.float32)
+        # the address of a device's current stream without a Stream object (3 us a call less)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
     return _dtypes
 
 
-class _on:
-    """The tensor's device as the current one for a call, and its current stream's address."""
+def _device_of(t, what: str):
+    """The tensor's CUDA device."""
+    if not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % what)
+    return t.device
 
-    def __init__(self, t, what: str):
-        if not t.is_cuda:
-            raise ValueError("%s must be on a CUDA device" % what)
-        import torch
-        self.device = t.device
-        self.index = t.device.index
-        self.torch = torch
 
-    def __enter__(self):
-        self.before = self.torch.cuda.current_device()
-        if self.before != self.index:
-            self.torch.cuda.set_device(self.index)
-        return self.torch.cuda.current_stream().cuda_stream
+def _run(device, call, *args):
+    """call(*args, stream) on the device and its current stream; the current device is the same afterwards."""
+    import torch
+    _torch_dtypes()
+    index = device.index
+    if torch.cuda.current_device() == index:
+        return call(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return call(*args, _raw_stream(index))
 
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            self.torch.cuda.set_device(self.before)
+
+def _addr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 class Routing:
@@ -274,7 +279,7 @@ class Routing:
     def __init__(self, router: "Router", T: int, device):
         import torch
         k, E = router.cfg.top_k, router.cfg.n_experts
-        self.T = T
+        self.size = (T, k, E)
         self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=device)
         self.topk_w = torch.empty((T, k), dtype=torch.float32, device=device)
         self.expert_offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
@@ -283,6 +288,12 @@ class Routing:
         self.inv_pos = torch.empty(T * k, dtype=torch.int32, device=device)
         n = ds4moe_route_logits_workspace(router.cfg, T)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+    @property
+    def addresses(self):
+        return (self.topk_idx.data_ptr(), self.topk_w.data_ptr(), self.expert_offsets.data_ptr(),
+                self.sorted_token.data_ptr(), self.sorted_slot.data_ptr(), self.inv_pos.data_ptr(),
+                _addr(self.workspace), 0 if self.workspace is None else self.workspace.numel())
 
 
 class Router:
@@ -301,30 +312,25 @@ class Router:
     def route(self, logits, bias=None, out: Optional[Routing] = None) -> Routing:
         """Routes the rows of logits [T, E] (rows may be strided); out: buffers of T tokens to write to."""
         T, E, ld = _rows_of(logits, "logits")
-        on = _on(logits, "logits")
+        device = _device_of(logits, "logits")
         code = _type_of(logits, "logits")
         if E != self.cfg.n_experts:
             raise ValueError("logits have %d columns for %d experts" % (E, self.cfg.n_experts))
-        _flat(bias, "float32", E, "bias", on.device)
+        _flat(bias, "float32", E, "bias", device)
         if out is None:
-            out = Routing(self, T, on.device)
-        elif out.T != T or out.topk_idx.shape[1] != self.cfg.top_k or out.expert_offsets.numel() != E + 1 or \
-                out.topk_idx.device != on.device:
+            out = Routing(self, T, device)
+        elif out.size != (T, self.cfg.top_k, E) or out.topk_idx.device != device:
             raise ValueError("out holds buffers of another size or device")
-        ws = out.workspace
-        with on as stream:
-            ds4moe_route_logits(self.cfg, logits, code, ld, T, bias, out.topk_idx, out.topk_w, out.expert_offsets,
-                                out.sorted_token, out.sorted_slot, out.inv_pos, ws, 0 if ws is None else ws.numel(),
-                                stream)
+        _check(_run(device, lib.ds4moe_route_logits, C.byref(self.cfg), logits.data_ptr(), code, ld,
+                    T, _addr(bias), *out.addresses), None, "ds4moe_route_logits")
         return out
 
 
 def mxfp4_quantize(x, inv_pos=None, codes=None, scales=None):
     """(codes, scales) of the rows of x; with inv_pos [rows, k] (int32) row r goes to rows inv_pos[r, j]
     of codes / scales (rows * k of them where they are not given)."""
-    import torch
     rows, K, ld = _rows_of(x, "x")
-    on = _on(x, "x")
+    device = _device_of(x, "x")
     code = _type_of(x, "x")
     if K == 0 or K % 32:
         raise ValueError("the rows of x must have a multiple of 32 elements")
@@ -333,59 +339,61 @@ def mxfp4_quantize(x, inv_pos=None, codes=None, scales=None):
         if inv_pos.dim() != 2 or inv_pos.shape[0] != rows:
             raise ValueError("inv_pos must have a row for each row of x")
         k = inv_pos.shape[1]
-        _flat(inv_pos, "int32", rows * k, "inv_pos", on.device)
+        _flat(inv_pos, "int32", rows * k, "inv_pos", device)
     if codes is None:
+        import torch
         codes = torch.empty((rows * k, K // 2), dtype=torch.uint8, device=x.device)
     out_rows = codes.shape[0]
     if scales is None:
+        import torch
         scales = torch.empty((out_rows, K // 32), dtype=torch.uint8, device=x.device)
-    _flat(codes, "uint8", out_rows * (K // 2), "codes", on.device)
-    _flat(scales, "uint8", out_rows * (K // 32), "scales", on.device)
-    with on as stream:
-        ds4moe_mxfp4_quantize(x, code, ld, rows, K, inv_pos, k, out_rows, codes, scales, stream)
+    _flat(codes, "uint8", out_rows * (K // 2), "codes", device)
+    _flat(scales, "uint8", out_rows * (K // 32), "scales", device)
+    _check(_run(device, lib.ds4moe_mxfp4_quantize, x.data_ptr(), code, ld, rows, K, _addr(inv_pos),
+                k, out_rows, codes.data_ptr(), scales.data_ptr()), None, "ds4moe_mxfp4_quantize")
     return codes, scales
 
 
 def mxfp4_dequantize(codes, scales, out=None):
     """The values of MXFP4 rows, in out (float32, bfloat16 or float16 [rows, K]; bfloat16 where it is not given,
     which holds every value but 2^-127 * 0.5 exactly)."""
-    import torch
     rows, half, _ = _rows_of(codes, "codes")
     K = 2 * half
-    on = _on(codes, "codes")
-    _flat(codes, "uint8", rows * half, "codes", on.device)
-    _flat(scales, "uint8", rows * (K // 32), "scales", on.device)
+    device = _device_of(codes, "codes")
+    _flat(codes, "uint8", rows * half, "codes", device)
+    _flat(scales, "uint8", rows * (K // 32), "scales", device)
     if out is None:
+        import torch
         out = torch.empty((rows, K), dtype=torch.bfloat16, device=codes.device)
     r, w, ld = _rows_of(out, "out")
-    if (r, w) != (rows, K) or out.device != on.device:
-        raise ValueError("out must be [%d, %d] on %s" % (rows, K, on.device))
-    with on as stream:
-        ds4moe_mxfp4_dequantize(codes, scales, rows, K, out, _type_of(out, "out"), ld, stream)
+    if (r, w) != (rows, K) or out.device != device:
+        raise ValueError("out must be [%d, %d] on %s" % (rows, K, device))
+    _check(_run(device, lib.ds4moe_mxfp4_dequantize, codes.data_ptr(), scales.data_ptr(), rows, K,
+                out.data_ptr(), _type_of(out, "out"), ld), None, "ds4moe_mxfp4_dequantize")
     return out
 
 
 def combine(o, inv_pos, topk_w, y=None, add=None):
     """y[t] = add[t] + sum_j topk_w[t, j] * o[inv_pos[t, j]] (a row outside o adds nothing); y is float32 where it
     is not given."""
-    import torch
     o_rows, H, ld = _rows_of(o, "o")
-    on = _on(o, "o")
+    device = _device_of(o, "o")
     if ld != H:
         raise ValueError("o must be contiguous")
     if topk_w.dim() != 2:
         raise ValueError("topk_w must be [T, k]")
     T, k = topk_w.shape
-    _flat(topk_w, "float32", T * k, "topk_w", on.device)
-    _flat(inv_pos, "int32", T * k, "inv_pos", on.device)
+    _flat(topk_w, "float32", T * k, "topk_w", device)
+    _flat(inv_pos, "int32", T * k, "inv_pos", device)
     if y is None:
+        import torch
         y = torch.empty((T, H), dtype=torch.float32, device=o.device)
     for t, what in ((y, "y"), (add, "add")):
-        if t is not None and (tuple(t.shape) != (T, H) or not t.is_contiguous() or t.device != on.device):
-            raise ValueError("%s must be a contiguous [%d, %d] tensor on %s" % (what, T, H, on.device))
-    with on as stream:
-        ds4moe_combine(o, _type_of(o, "o"), o_rows, T, k, H, inv_pos, topk_w, add,
-                       0 if add is None else _type_of(add, "add"), y, _type_of(y, "y"), stream)
+        if t is not None and (t.shape != (T, H) or not t.is_contiguous() or t.device != device):
+            raise ValueError("%s must be a contiguous [%d, %d] tensor on %s" % (what, T, H, device))
+    _check(_run(device, lib.ds4moe_combine, o.data_ptr(), _type_of(o, "o"), o_rows, T, k, H,
+                inv_pos.data_ptr(), topk_w.data_ptr(), _addr(add), 0 if add is None else _type_of(add, "add"), y.data_ptr(),
+                _type_of(y, "y")), None, "ds4moe_combine")
     return y
 
 
@@ -413,50 +421,51 @@ class Mxfp4Experts:
         except Exception:
             pass
 
-    def _on(self, t, what):
-        on = _on(t, what)
-        if on.index != self.device:
-            raise ValueError("%s is on %s, the experts on device %d" % (what, on.device, self.device))
-        return on
+    def _device_of(self, t, what):
+        device = _device_of(t, what)
+        if device.index != self.device:
+            raise ValueError("%s is on %s, the experts on device %d" % (what, device, self.device))
+        return device
 
     def load(self, codes, scales, up_codes=None, up_scales=None):
         """codes uint8 [E, n_out, n_in / 2] and scales uint8 [E, n_out, n_in / 32] on the device; a gated projection
         takes the gate's and the up matrix's."""
         if (up_codes is None) != (up_scales is None) or (up_codes is not None) != self.gated:
             raise ValueError("a gated projection takes two matrices, another takes one")
-        on = self._on(codes, "codes")
+        device = self._device_of(codes, "codes")
         n = self.n_experts * self.n_out
         for t, per, what in ((codes, self.n_in // 2, "codes"), (scales, self.n_in // 32, "scales"),
                              (up_codes, self.n_in // 2, "up_codes"), (up_scales, self.n_in // 32, "up_scales")):
-            _flat(t, "uint8", n * per, what, on.device)
-        with on as stream:
-            ds4moe_mxfp4_load(self.h, codes, scales, up_codes, up_scales, stream)
+            _flat(t, "uint8", n * per, what, device)
+        _check_mxfp4(_run(device, lib.ds4moe_mxfp4_load, self.h, codes.data_ptr(), scales.data_ptr(),
+                          _addr(up_codes), _addr(up_scales)), self.h, "ds4moe_mxfp4_load")
 
     def product(self, a_codes, a_scales, offsets=None, out=None, out_scales=None):
         """Rows of a [rows, n_in] in MXFP4, grouped by offsets int32 [E + 1] (None for one expert), times their
         experts' matrices.  out: [rows, n_out] of float32, bfloat16 (where it is not given) or float16, rows may be
         strided; or uint8 [rows, n_out / 2] with out_scales uint8 [rows, n_out / 32] for MXFP4."""
-        import torch
         rows, half, _ = _rows_of(a_codes, "a_codes")
-        on = self._on(a_codes, "a_codes")
+        device = self._device_of(a_codes, "a_codes")
         if half * 2 != self.n_in:
             raise ValueError("a_codes has rows of %d inputs, the experts take %d" % (half * 2, self.n_in))
-        _flat(a_codes, "uint8", rows * half, "a_codes", on.device)
-        _flat(a_scales, "uint8", rows * (self.n_in // 32), "a_scales", on.device)
-        _flat(offsets, "int32", self.n_experts + 1, "offsets", on.device)
+        _flat(a_codes, "uint8", rows * half, "a_codes", device)
+        _flat(a_scales, "uint8", rows * (self.n_in // 32), "a_scales", device)
+        _flat(offsets, "int32", self.n_experts + 1, "offsets", device)
         if out is None:
+            import torch
             out = torch.empty((rows, self.n_out), dtype=torch.bfloat16, device=a_codes.device)
         if out_scales is not None:
-            _flat(out, "uint8", rows * (self.n_out // 2), "out", on.device)
-            _flat(out_scales, "uint8", rows * (self.n_out // 32), "out_scales", on.device)
+            _flat(out, "uint8", rows * (self.n_out // 2), "out", device)
+            _flat(out_scales, "uint8", rows * (self.n_out // 32), "out_scales", device)
             code, ld = MXFP4, self.n_out
         else:
             r, n, ld = _rows_of(out, "out")
-            if (r, n) != (rows, self.n_out) or out.device != on.device:
-                raise ValueError("out must be [%d, %d] on %s" % (rows, self.n_out, on.device))
+            if (r, n) != (rows, self.n_out) or out.device != device:
+                raise ValueError("out must be [%d, %d] on %s" % (rows, self.n_out, device))
             code = _type_of(out, "out")
-        with on as stream:
-            ds4moe_mxfp4_product(self.h, a_codes, a_scales, rows, offsets, out, code, ld, out_scales, stream)
+        _check_mxfp4(_run(device, lib.ds4moe_mxfp4_product, self.h, a_codes.data_ptr(),
+                          a_scales.data_ptr(), rows, _addr(offsets), out.data_ptr(), code, ld, _addr(out_scales)), self.h,
+                     "ds4moe_mxfp4_product")
         return out
 
     def sync_status(self):
