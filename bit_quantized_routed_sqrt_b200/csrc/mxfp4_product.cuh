@@ -17,7 +17,6 @@ struct MxArgs {
     uint8_t *out_scales;       // MXFP4 output
     int out_type;
     int64_t ld;                // elements between output rows (MXFP4: packed, ld = N)
-    int vec_out;               // 16-byte stores are aligned
     int *status;
 };
 
@@ -39,14 +38,22 @@ __device__ __forceinline__ void mx_group(const MxArgs &p, int e, int &first, int
 //   warp 1     allocates tensor memory; copies the step's scales there (tcgen05.cp) and issues
 //              the MMAs.  Every stage has its own scale columns, so a copy never meets an MMA
 //              that still reads the columns' last contents
-//   warp 2     rows' scales: plain loads (rows start anywhere, K / 32 is any number), laid out
-//              in shared memory as the copy wants them
-//   warps 4-7  epilogue: accumulators -> silu(g) * u -> shared memory -> rows of the output
+//   warp 2     rows' scales (rows start anywhere, K / 32 is any number), laid out in shared
+//              memory as the copy wants them
+//   warps 4-11 epilogue, in two groups of four that take chunks of 32 rows in turn: accumulators
+//              -> silu(g) * u -> output.  A lane is an output, so a warp stores 32 (gated: two
+//              times 16) neighbouring elements of a row at once; staging 128-byte rows in shared
+//              memory with four warps kept the tensor pipe waiting (1.13 ms against XXX at 65536
+//              rows x 7168 x 2048)
 // The accumulators are double buffered, so a tile's epilogue overlaps the next tile.
 // Every wait is bounded, as in the layer's grouped GEMM: on a timeout the CTA records
 // ETIMEOUT, waits for its own copies and MMAs, frees tensor memory and returns.
-constexpr int MX_THREADS = 256;
-constexpr int MX_CHUNK = 32;             // rows of a that pass through shared memory at a time
+constexpr int MX_THREADS = 384;
+constexpr int MX_SF_AHEAD = 3;           // steps of row scales in flight
+constexpr int MX_CHUNK = 32;             // rows of a (accumulator columns) that an epilogue warp takes at a time
+// MXFP4 output: of each pair of epilogue warps, two buffers of the codes of 32 rows x 32
+// outputs and of each warp's largest magnitudes
+constexpr int MX_PAIR_BYTES = 2 * (32 * 16 + 2 * 32 * 4);
 
 template <int NT_, int BOX_, int STAGES_, bool GATED_>
 struct MxCfg {
@@ -62,11 +69,11 @@ struct MxCfg {
     static constexpr int COLS = 2 * NT + STAGES * SF_COLS;
     static constexpr int TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static constexpr int F = GATED ? 64 : 128;                         // outputs of a tile
-    static constexpr int PITCH = F + 4;                                // floats between rows of the epilogue buffer
-    static constexpr int EPI_BYTES = MX_CHUNK * PITCH * 4;
+    static constexpr int EPI_BYTES = 4 * MX_PAIR_BYTES;
     static constexpr int S_BYTES = (SR_MAX_EXPERTS + 1) * 4;
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + 512 + S_BYTES;
     static_assert(COLS <= 512, "tensor memory");
+    static_assert(STAGES > MX_SF_AHEAD, "scales in flight");
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
     static_assert(NT % 16 == 0 && NT % BOX == 0 && BOX % 8 == 0, "row tiles");
 };
@@ -117,16 +124,91 @@ __device__ __forceinline__ MxTile mx_tile(const MxArgs &p, const int *S, int64_t
     return x;
 }
 
-// y (8 consecutive outputs of row r from output f) -> the output, plain types.
-template <class T>
-__device__ __forceinline__ void mx_store8(const MxArgs &p, size_t o, int f, const float (&y)[8], bool vec) {
-    T *out = reinterpret_cast<T *>(p.out) + o;
-    if (vec && f + 8 <= p.N) {
-        store_row<T, 8, true>(out, y);
+__device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + expf(-g)); }
+
+// One chunk of an epilogue warp: rows row0 .. row0 + rows - 1 (rows <= 32) from accumulator
+// columns v, outputs from f0 on (this warp's: 32, gated 16).
+template <bool GATED, class T>
+__device__ __forceinline__ void mx_store_chunk(const MxArgs &p, const float (&v)[32], size_t row0, int rows, int f0) {
+    const int lane = threadIdx.x & 31;
+    const int f = f0 + (GATED ? lane >> 1 : lane);
+    T *out = reinterpret_cast<T *>(p.out) + (row0 + (GATED ? lane & 1 : 0)) * p.ld + f;
+    const bool mine = f < p.N;
+    if (GATED) {
+        // lane 2i holds gate i, lane 2i + 1 up i: the even lane takes row j, the odd one row j + 1
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[j] : v[j + 1], 1);
+            const float g = (lane & 1) ? got : v[j], u = (lane & 1) ? v[j + 1] : got;
+            if (mine && j + (lane & 1) < rows) out[j * p.ld] = from_f32<T>(silu_fast(g) * u);
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (f + j < p.N) out[j] = from_f32<T>(y[j]);
+        for (int j = 0; j < 32; ++j)
+            if (mine && j < rows) out[j * p.ld] = from_f32<T>(v[j]);
+    }
+}
+
+// The same for MXFP4 output.  Gated, a pair of warps holds the 32 outputs of a block, 16 each
+// (half: which): they exchange their largest magnitudes and put their codes into one buffer,
+// at two barriers of the pair; otherwise a warp holds a whole block and uses a buffer alone.
+template <bool GATED>
+__device__ __forceinline__ void mx_store_chunk_mxfp4(const MxArgs &p, const float (&v)[32], size_t row0, int rows, int f0,
+                                                     uint8_t *buf, int bar, int half) {
+    const int lane = threadIdx.x & 31;
+    uint8_t *codes = buf;                                        // [32 rows][16]
+    uint32_t *amaxs = reinterpret_cast<uint32_t *>(buf + 512);   // [2][32 rows]
+    if (GATED) {
+        float h[16];
+        uint32_t m[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[2 * j] : v[2 * j + 1], 1);
+            const float g = (lane & 1) ? got : v[2 * j], u = (lane & 1) ? v[2 * j + 1] : got;
+            h[j] = silu_fast(g) * u;
+            m[j] = __float_as_uint(h[j]) & 0x7fffffffu;
+        }
+#pragma unroll
+        for (int o = 2; o < 32; o <<= 1)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) m[j] = max(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
+        if (lane < 2)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) amaxs[half * 32 + 2 * j + lane] = m[j];
+        asm volatile("barrier.cta.sync %0, 64;" ::"r"(bar) : "memory");
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int r = 2 * j + (lane & 1);
+            const uint32_t s = mx_scale_byte(max(m[j], amaxs[(half ^ 1) * 32 + r]));
+            const float y = s == 255u ? 6.0f : h[j] * mx_inverse(s);
+            const float next = __shfl_xor_sync(0xffffffffu, y, 2);
+            if ((lane & 2) == 0) codes[r * 16 + half * 8 + (lane >> 2)] = (uint8_t)e2m1x2_code(y, next);
+        }
+        asm volatile("barrier.cta.sync %0, 64;" ::"r"(bar) : "memory");
+        if (half == 0 && lane < rows && f0 < p.N) {
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(p.out) + (row0 + lane) * (p.N / 2) + f0 / 2) =
+                *reinterpret_cast<const uint4 *>(codes + lane * 16);
+        } else if (half == 1 && lane < rows && f0 - 16 < p.N) {
+            p.out_scales[(row0 + lane) * (p.N / MX_BLOCK) + (f0 - 16) / MX_BLOCK] =
+                (uint8_t)mx_scale_byte(max(amaxs[lane], amaxs[32 + lane]));
+        }
+    } else {
+        uint32_t my_scale = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const uint32_t s = mx_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu));
+            const float y = s == 255u ? 6.0f : v[j] * mx_inverse(s);
+            const float next = __shfl_xor_sync(0xffffffffu, y, 1);
+            if ((lane & 1) == 0) codes[j * 16 + (lane >> 1)] = (uint8_t)e2m1x2_code(y, next);
+            if (lane == j) my_scale = s;
+        }
+        __syncwarp();
+        if (lane < rows && f0 < p.N) {
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(p.out) + (row0 + lane) * (p.N / 2) + f0 / 2) =
+                *reinterpret_cast<const uint4 *>(codes + lane * 16);
+            p.out_scales[(row0 + lane) * (p.N / MX_BLOCK) + f0 / MX_BLOCK] = (uint8_t)my_scale;
+        }
+        __syncwarp();
     }
 }
 
@@ -134,8 +216,8 @@ template <class C>
 __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __grid_constant__ CUtensorMap tm_a, MxArgs p) {
     extern __shared__ __align__(1024) uint8_t mx_smem_raw[];
     uint8_t *stages = mx_smem_raw + ((1024u - (smem_u32(mx_smem_raw) & 1023u)) & 1023u);
-    float *epi = reinterpret_cast<float *>(stages + C::STAGES * C::STAGE_BYTES);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(epi) + C::EPI_BYTES);
+    uint8_t *epi = stages + C::STAGES * C::STAGE_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(epi + C::EPI_BYTES);
     uint64_t *full = bars;                       // [S] producer (with the bytes) and the scale warp
     uint64_t *empty = full + C::STAGES;          // [S] MMA commit
     uint64_t *acc_full = empty + C::STAGES;      // [2] MMA commit
@@ -155,7 +237,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __gr
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(acc_full + b), 1);
-            mbar_init(smem_u32(acc_empty + b), 4);
+            mbar_init(smem_u32(acc_empty + b), 8);
         }
         mbar_init(smem_u32(drain), 1);
         *abort = 0;
@@ -217,7 +299,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __gr
             if (!(ok = mbar_wait(smem_u32(acc_empty + b), ((tc >> 1) & 1) ^ 1, abort, p.status))) break;
             tc_fence_after();
             const int N = (x.n + 15) & ~15;
-            const int chunks = (N + 127) >> 7;
+            const uint32_t idesc0 = mxf4_idesc(N, 0), idesc2 = mxf4_idesc(N, 2);
             const uint32_t d = tmem + b * C::NT;
             for (int kt = 0; kt < KT; ++kt, ++it) {
                 const uint32_t s = it % C::STAGES;
@@ -226,15 +308,21 @@ __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __gr
                 const uint32_t st = smem_u32(stages + s * C::STAGE_BYTES);
                 const uint32_t sfa = tmem + 2 * C::NT + s * C::SF_COLS, sfb = sfa + 8;
                 const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + C::B_OFF);
-                const int steps = min(4, (p.K - kt * MX_TK + 63) >> 6);
                 if (elect_one()) {
-                    for (int g = 0; g < (steps + 1) / 2; ++g) {
+                    // Unrolled, with every operand a constant off the step's base: a loop with
+                    // run-time bounds moved each instruction's operands to uniform registers
+                    // one by one and took 1000 cycles a step where the MMAs take 260 to 510.
+                    // Inputs past K are zeros, so the last step runs whole as well.
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
                         mx_copy_scales(sfa + 4 * g, st + MX_CODE_BYTES + 512 * g);
-                        for (int c = 0; c < chunks; ++c)
+#pragma unroll
+                        for (int c = 0; c < C::SF_CHUNKS; ++c)
                             mx_copy_scales(sfb + 4 * (g * C::SF_CHUNKS + c), st + MX_TILE_BYTES + 512 * (g * C::SF_CHUNKS + c));
                     }
-                    for (int kk = 0; kk < steps; ++kk)
-                        mx_mma(d, ad + 2 * kk, bd + 2 * kk, mxf4_idesc(N, 2 * (kk & 1)), sfa + 4 * (kk >> 1),
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mx_mma(d, ad + 2 * kk, bd + 2 * kk, kk & 1 ? idesc2 : idesc0, sfa + 4 * (kk >> 1),
                                sfb + 4 * C::SF_CHUNKS * (kk >> 1), (kt | kk) != 0);
                     tc_commit(smem_u32(empty + s));
                 }
@@ -248,138 +336,117 @@ __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __gr
         mbar_drain(smem_u32(drain), 0, p.status);
     } else if (warp == 2) {
         // ----------------------------------------------------------------- row scales
-        // Chunk (g, c) of a stage: lane l holds the four bytes of rows 128 c + 32 j + l, j < 4.
-        // A step's words are loaded one step ahead of their stage.
-        constexpr int WORDS = 2 * 4 * C::SF_CHUNKS;
+        // Chunk (g, c) of a stage: 16 bytes for each l < 32, the four bytes of rows
+        // 128 c + 32 j + l, j < 4.  Words come by asynchronous copies (zeros for rows that are
+        // not the tile's), up to MX_SF_AHEAD steps in flight: with one step of register
+        // prefetch every K step took an L2 round trip (1.13 ms against XXX at 65536 rows x
+        // 7168 x 2048).  K / 32 not a multiple of four leaves words unaligned: bytes then.
         const int kb = p.K / MX_BLOCK;
-        const bool wide = kb % 8 == 0 && ((uintptr_t)p.a_scales & 7) == 0;
-        uint32_t w[WORDS];
-        auto load = [&](const MxTile &x, int kt) {
-#pragma unroll
-            for (int j = 0; j < WORDS / 2; ++j) {
-                const int r = 32 * j + lane;
-                uint32_t v[2] = {0x7f7f7f7fu, 0x7f7f7f7fu};
-                if (r < x.n) {
-                    const uint8_t *src = p.a_scales + (size_t)(x.row0 + r) * kb + kt * 8;
-                    if (wide) {
-                        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
-                        v[0] = u.x;
-                        v[1] = u.y;
-                    } else {
-                        for (int i = 0; i < 8 && kt * 8 + i < kb; ++i)
-                            v[i >> 2] = (v[i >> 2] & ~(0xffu << (8 * (i & 3)))) | ((uint32_t)__ldg(src + i) << (8 * (i & 3)));
-                    }
-                }
-                w[j] = v[0];
-                w[WORDS / 2 + j] = v[1];
-            }
-        };
         uint32_t it = 0;
         bool ok = true;
-        int64_t t = blockIdx.x;
-        MxTile x{};
-        if (t < tiles) {
-            x = mx_tile(p, S, t, MT, C::NT);
-            load(x, 0);
-        }
-        int kt = 0;
-        while (t < tiles) {
-            const uint32_t s = it % C::STAGES;
-            if (!(ok = mbar_wait(smem_u32(empty + s), ((it / C::STAGES) & 1) ^ 1, abort, p.status))) break;
-            const uint32_t dst = smem_u32(stages + s * C::STAGE_BYTES) + MX_TILE_BYTES + lane * 16;
+        if (kb % 4 == 0 && ((uintptr_t)p.a_scales & 3) == 0) {
+            uint32_t pending = 0;   // the last steps whose copies may be in flight
+            auto publish = [&](uint32_t n) {   // the n oldest of them have landed
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0)
+                    for (uint32_t i = it - pending; i < it - pending + n; ++i) mbar_arrive(smem_u32(full + i % C::STAGES));
+                pending -= n;
+            };
+            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const MxTile x = mx_tile(p, S, t, MT, C::NT);
+                const uint8_t *src = p.a_scales + (size_t)(x.row0 + lane) * kb;
+                for (int kt = 0; kt < KT; ++kt) {
+                    const uint32_t s = it % C::STAGES, bar = smem_u32(empty + s), parity = ((it / C::STAGES) & 1) ^ 1;
+                    if (!__all_sync(0xffffffffu, mbar_try_spin(bar, parity))) {
+                        // no free stage: hand over what there is meanwhile
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                        publish(pending);
+                        if (!(ok = mbar_wait(bar, parity, abort, p.status))) break;
+                    }
+                    const uint32_t dst = smem_u32(stages + s * C::STAGE_BYTES) + MX_TILE_BYTES + lane * 16;
 #pragma unroll
-            for (int c = 0; c < WORDS / 4; ++c)
-                sts_v4(dst + 512 * c, make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(full + s));
-            ++it;
-            if (++kt == KT) {
-                kt = 0;
-                t += gridDim.x;
-                if (t >= tiles) break;
-                x = mx_tile(p, S, t, MT, C::NT);
+                    for (int j = 0; j < 4 * C::SF_CHUNKS; ++j) {
+                        if (32 * j >= C::NT) break;
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                                             dst + 512 * (g * C::SF_CHUNKS + j / 4) + 4 * (j & 3)),
+                                         "l"(32 * j + lane < x.n && kt * 8 + 4 * g < kb ? src + (size_t)32 * j * kb + kt * 8 + 4 * g : p.a_scales),
+                                         "r"(32 * j + lane < x.n && kt * 8 + 4 * g < kb ? 4 : 0)
+                                         : "memory");
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    ++it;
+                    if (++pending > MX_SF_AHEAD) {
+                        asm volatile("cp.async.wait_group %0;" ::"n"(MX_SF_AHEAD) : "memory");
+                        publish(1);
+                    }
+                }
             }
-            load(x, kt);
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            publish(pending);
+        } else {
+            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const MxTile x = mx_tile(p, S, t, MT, C::NT);
+                for (int kt = 0; kt < KT; ++kt, ++it) {
+                    const uint32_t s = it % C::STAGES;
+                    if (!(ok = mbar_wait(smem_u32(empty + s), ((it / C::STAGES) & 1) ^ 1, abort, p.status))) break;
+                    uint8_t *dst = stages + s * C::STAGE_BYTES + MX_TILE_BYTES;
+                    for (int i = lane; i < 8 * x.n; i += 32) {
+                        const int r = i >> 3, blk = i & 7;
+                        dst[512 * ((blk >> 2) * C::SF_CHUNKS + r / 128) + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (blk & 3)] =
+                            kt * 8 + blk < kb ? __ldg(p.a_scales + (size_t)(x.row0 + r) * kb + kt * 8 + blk) : 0;
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(full + s));
+                }
+            }
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------------- epilogue
-        const int q = warp - 4, et = threadIdx.x - 128;
-        const bool vec = p.vec_out != 0;
-        uint32_t tc = 0;
+        const int q = warp & 3, group = (warp - 4) >> 2, pair = group * 2 + (q >> 1);
+        uint8_t *pair_buf = epi + pair * MX_PAIR_BYTES;
+        const int bar = 1 + pair;
+        uint32_t tc = 0, used = 0;
         for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
             const MxTile x = mx_tile(p, S, t, MT, C::NT);
             const uint32_t b = tc & 1;
-            // the four warps leave together: they meet at barriers below
+            // the two warps of a pair leave together: they meet at barriers in their chunks
             uint32_t ok = mbar_wait(smem_u32(acc_full + b), (tc >> 1) & 1, abort, p.status, nullptr, 0, 0, 64);
-            asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %0, 0;\n\tbarrier.cta.red.and.pred b, 1, 128, a;\n\t"
-                         "selp.u32 %0, 1, 0, b;\n\t}" : "+r"(ok)::"memory");
+            asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %0, 0;\n\tbarrier.cta.red.and.pred b, %1, 64, a;\n\t"
+                         "selp.u32 %0, 1, 0, b;\n\t}" : "+r"(ok) : "r"(bar) : "memory");
             if (!ok) break;
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * C::NT;
-            for (int c0 = 0; c0 < x.n; c0 += MX_CHUNK) {
+            const int f0 = x.m * C::F + q * (C::F / 4);
+            const int chunks = (x.n + MX_CHUNK - 1) / MX_CHUNK;
+            const int first = (group ^ tc) & 1;   // a tile of one chunk goes to either group in turn
+            for (int c = first; c < chunks; c += 2) {
                 float v[32];
-                tc_ld32(acc + c0, v);
+                tc_ld32(acc + c * MX_CHUNK, v);
                 tc_wait_ld();
-                if (c0 + MX_CHUNK >= x.n) {   // the tile's last columns are read
+                if (c + 2 >= chunks) {   // this warp's last columns are read
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(acc_empty + b));
                 }
-                if (C::GATED) {
-                    // lane 2i holds gate i, lane 2i + 1 up i: the even lane takes row j, the odd one row j + 1
-                    float *dst = epi + (lane & 1) * C::PITCH + q * 16 + (lane >> 1);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[j] : v[j + 1], 1);
-                        const float g = (lane & 1) ? got : v[j], u = (lane & 1) ? v[j + 1] : got;
-                        dst[j * C::PITCH] = silu(g) * u;
-                    }
-                } else {
-                    float *dst = epi + q * 32 + lane;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) dst[j * C::PITCH] = v[j];
+                const size_t row0 = (size_t)x.row0 + c * MX_CHUNK;
+                const int rows = min(MX_CHUNK, x.n - c * MX_CHUNK);
+                if (p.out_type == DT_F32) mx_store_chunk<C::GATED, float>(p, v, row0, rows, f0);
+                else if (p.out_type == DT_BF16) mx_store_chunk<C::GATED, __nv_bfloat16>(p, v, row0, rows, f0);
+                else if (p.out_type == DT_F16) mx_store_chunk<C::GATED, __half>(p, v, row0, rows, f0);
+                else {
+                    // gated: the pair's buffers in turn; else each warp its own
+                    const uint32_t which = C::GATED ? used & 1 : q & 1;
+                    mx_store_chunk_mxfp4<C::GATED>(p, v, row0, rows, f0, pair_buf + which * (MX_PAIR_BYTES / 2), bar, q & 1);
+                    ++used;
                 }
-                asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-                const int rows = min(MX_CHUNK, x.n - c0);
-                // items of 8 outputs of a row, a row's items on consecutive threads
-                for (int i = et; i < rows * (C::F / 8); i += 128) {
-                    const int r = i / (C::F / 8), g8 = i % (C::F / 8), f = x.m * C::F + g8 * 8;
-                    float y[8];
-                    const float4 y0 = *reinterpret_cast<const float4 *>(epi + r * C::PITCH + g8 * 8);
-                    const float4 y1 = *reinterpret_cast<const float4 *>(epi + r * C::PITCH + g8 * 8 + 4);
-                    y[0] = y0.x; y[1] = y0.y; y[2] = y0.z; y[3] = y0.w;
-                    y[4] = y1.x; y[5] = y1.y; y[6] = y1.z; y[7] = y1.w;
-                    const size_t row = (size_t)x.row0 + c0 + r;
-                    if (p.out_type == DT_MXFP4) {
-                        // four threads hold a block of 32 outputs (rows * F / 8 is a multiple of 8)
-                        uint32_t amax = 0;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(y[j]) & 0x7fffffffu);
-                        const unsigned team = 0xfu << (threadIdx.x & 28);
-                        amax = max(amax, __shfl_xor_sync(team, amax, 1));
-                        amax = max(amax, __shfl_xor_sync(team, amax, 2));
-                        const uint32_t sc = mx_scale_byte(amax);
-                        uint32_t c = 0x77777777u;
-                        if (sc != 255u) {
-                            const float inv = mx_inverse(sc);
-                            c = 0;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) c |= e2m1x2_code(y[2 * j] * inv, y[2 * j + 1] * inv) << (8 * j);
-                        }
-                        if (f < p.N) {   // N % 32 == 0: a block is all in or all out
-                            *reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(p.out) + row * (p.N / 2) + f / 2) = c;
-                            if ((g8 & 3) == 0) p.out_scales[row * (p.N / MX_BLOCK) + f / MX_BLOCK] = (uint8_t)sc;
-                        }
-                    } else if (p.out_type == DT_F32) {
-                        mx_store8<float>(p, row * p.ld + f, f, y, vec);
-                    } else if (p.out_type == DT_BF16) {
-                        mx_store8<__nv_bfloat16>(p, row * p.ld + f, f, y, vec);
-                    } else {
-                        mx_store8<__half>(p, row * p.ld + f, f, y, vec);
-                    }
-                }
-                asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+            }
+            if (first >= chunks) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(acc_empty + b));
             }
         }
     }

@@ -131,7 +131,7 @@ ds4moe_status pick_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
     const double per_expert = (double)a.rows / std::min(a.rows, a.E);
     if (per_expert <= 24) return run_product<MxCfg<32, 8, 8, GATED>>(h, a, st);
     if (per_expert <= 112) return run_product<MxCfg<128, 32, 5, GATED>>(h, a, st);
-    return run_product<MxCfg<192, 32, 4, GATED>>(h, a, st);
+    return run_product<MxCfg<192, 32, 5, GATED>>(h, a, st);
 }
 
 }  // namespace
@@ -356,7 +356,6 @@ ds4moe_status ds4moe_mxfp4_product(ds4moe_mxfp4 *h, const uint8_t *a_codes_dev, 
     a.a_codes = a_codes_dev; a.a_scales = a_scales_dev; a.rows = rows; a.offsets = expert_offsets_dev;
     a.out = out_dev; a.out_scales = out_scales_dev; a.out_type = out_type; a.ld = ld;
     a.status = h->status;
-    a.vec_out = out_type != DS4MOE_MXFP4 && aligned16(out_dev) && ld * size_of(out_type) % 16 == 0;
     return g.gated ? pick_product<true>(h, a, st) : pick_product<false>(h, a, st);
 }
 
