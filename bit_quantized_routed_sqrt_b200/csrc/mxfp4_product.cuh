@@ -31,10 +31,10 @@ __device__ __forceinline__ void mx_group(const MxArgs &p, int e, int &first, int
 // to NT rows of a (the MMA's N): each expert's rows are cut into equal tiles of at most NT, and
 // the tiles that share weight rows follow one another, so the weights cross HBM once.  One
 // K step is 256 inputs: a weight tile with its scales (one contiguous bulk copy), the rows'
-// codes (TMA, 128-byte swizzle, only the boxes that hold rows of the tile) and the rows'
+// codes (TMA, 128-byte swizzle) and the rows'
 // scales, then four block-scaled MMAs of 64 inputs (kind::mxf4, E2M1 x E2M1 with an E8M0 scale
 // per 32, exact products, fp32 accumulators in tensor memory).
-//   warp 0     producer of weight tiles and row codes
+//   warps 0, 3 producers of weight tiles and of row codes
 //   warp 1     allocates tensor memory; copies the step's scales there (tcgen05.cp) and issues
 //              the MMAs.  Every stage has its own scale columns, so a copy never meets an MMA
 //              that still reads the columns' last contents
@@ -52,12 +52,13 @@ constexpr int MX_THREADS = 384;
 constexpr int MX_SF_AHEAD = 3;           // steps of row scales in flight
 constexpr int MX_CHUNK = 32;             // rows of a (accumulator columns) that an epilogue warp takes at a time
 // MXFP4 output: of each pair of epilogue warps, two buffers of the codes of 32 rows x 32
-// outputs and of each warp's largest magnitudes
-constexpr int MX_PAIR_BYTES = 2 * (32 * 16 + 2 * 32 * 4);
+// outputs and of each warp's scale bytes
+constexpr int MX_PAIR_BYTES = 2 * (32 * 16 + 2 * 32);
 
-template <int NT_, int BOX_, int STAGES_, bool GATED_>
+// BOX1 < BOX0 < NT: the row counts that one TMA load can bring (a tile takes the least that holds it).
+template <int NT_, int BOX0_, int BOX1_, int STAGES_, bool GATED_>
 struct MxCfg {
-    static constexpr int NT = NT_, BOX = BOX_, STAGES = STAGES_;
+    static constexpr int NT = NT_, BOX0 = BOX0_, BOX1 = BOX1_, STAGES = STAGES_;
     static constexpr bool GATED = GATED_;
     static constexpr int SF_CHUNKS = (NT + 127) / 128;                 // 512-byte scale chunks of the rows per 128 inputs
     static constexpr int B_BYTES = (NT * 128 + 1023) / 1024 * 1024;
@@ -70,12 +71,14 @@ struct MxCfg {
     static constexpr int TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static constexpr int F = GATED ? 64 : 128;                         // outputs of a tile
     static constexpr int EPI_BYTES = 4 * MX_PAIR_BYTES;
-    static constexpr int S_BYTES = (SR_MAX_EXPERTS + 1) * 4;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + 512 + S_BYTES;
+    static constexpr int BAR_BYTES = 256;
+    static constexpr int S_BYTES = 3 * (SR_MAX_EXPERTS + 1) * 4;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES + S_BYTES;
     static_assert(COLS <= 512, "tensor memory");
     static_assert(STAGES > MX_SF_AHEAD, "scales in flight");
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
-    static_assert(NT % 16 == 0 && NT % BOX == 0 && BOX % 8 == 0, "row tiles");
+    static_assert(NT % 16 == 0 && NT > BOX0 && BOX0 > BOX1 && BOX1 % 8 == 0, "row tiles");
+    static_assert((2 * STAGES + 5) * 8 + 16 + 32 <= BAR_BYTES, "barrier area");
 };
 
 // Instruction descriptor of kind::mxf4: E2M1 A and B (K-major), E8M0 scales, fp32 D, M = 128, N;
@@ -102,27 +105,48 @@ struct MxTile {
     int e, m, row0, n;   // expert, weight row tile, first row of a, rows
 };
 
-// Tile t: S[e] counts the row tiles of the experts before e.
-__device__ __forceinline__ MxTile mx_tile(const MxArgs &p, const int *S, int64_t t, int MT, int NT) {
-    const int u = (int)(t / MT);
-    int lo = 0, hi = p.E;   // S[lo] <= u < S[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (S[mid] <= u) lo = mid; else hi = mid;
+// The tiles of one CTA in order, for one warp: S[e] counts the row tiles of the experts before
+// e, lo[e] and hi[e] are its rows, MT is the number of weight row tiles.  Tiles and their
+// counts fit 31 bits (the host checks).
+template <int NT>
+struct MxTiles {
+    const int *S, *row_lo, *row_hi;
+    uint32_t MT, t, tiles, lo, hi;   // the expert's tiles: [lo, hi)
+    int E, e, nt, first, last, per;
+
+    __device__ __forceinline__ MxTiles(const int *S_, int E_, int MT_, uint32_t tiles_)
+        : S(S_), row_lo(S_ + SR_MAX_EXPERTS + 1), row_hi(S_ + 2 * (SR_MAX_EXPERTS + 1)), MT(MT_), t(blockIdx.x),
+          tiles(tiles_), lo(0), hi(0), E(E_), e(-1) {}
+    __device__ __forceinline__ bool more() const { return t < tiles; }
+    __device__ __forceinline__ void next() { t += gridDim.x; }
+    __device__ __forceinline__ MxTile get() {
+        if (t >= hi) {
+            // The last expert behind e with S * MT <= t, 32 candidates at a time: it is E - 1 at
+            // most, and S[e + 1] * MT <= t holds (the tiles of e end there).
+            const int lane = threadIdx.x & 31;
+            int l = e + 1;
+            const int step = (E - l + 31) >> 5;   // at most 16
+            int i = l + lane * step;
+            l += (__popc(__ballot_sync(0xffffffffu, i < E && (uint32_t)S[min(i, E)] * MT <= t)) - 1) * step;
+            i = l + lane;
+            l += __popc(__ballot_sync(0xffffffffu, lane < step && i < E && (uint32_t)S[min(i, E)] * MT <= t)) - 1;
+            e = l;
+            lo = (uint32_t)S[e] * MT;
+            nt = S[e + 1] - S[e];
+            hi = lo + nt * MT;
+            first = row_lo[e];
+            last = row_hi[e];
+            per = min(NT, ((last - first + nt - 1) / nt + 15) & ~15);
+        }
+        MxTile x;
+        x.e = e;
+        const uint32_t local = t - lo;
+        x.m = nt == 1 ? local : local / (uint32_t)nt;
+        x.row0 = first + (int)(local - (uint32_t)x.m * nt) * per;
+        x.n = min(per, last - x.row0);   // at least 1: nt tiles of per rows are needed
+        return x;
     }
-    MxTile x;
-    x.e = lo;
-    const int s0 = S[lo], nt = S[lo + 1] - s0;
-    const int64_t local = t - (int64_t)s0 * MT;
-    x.m = (int)(local / nt);
-    const int i = (int)(local - (int64_t)x.m * nt);
-    int first, last;
-    mx_group(p, lo, first, last);
-    const int per = min(NT, ((last - first + nt - 1) / nt + 15) & ~15);
-    x.row0 = first + i * per;
-    x.n = min(per, last - x.row0);   // at least 1: nt tiles of per rows are needed
-    return x;
-}
+};
 
 __device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + expf(-g)); }
 
@@ -133,31 +157,41 @@ __device__ __forceinline__ void mx_store_chunk(const MxArgs &p, const float (&v)
     const int lane = threadIdx.x & 31;
     const int f = f0 + (GATED ? lane >> 1 : lane);
     T *out = reinterpret_cast<T *>(p.out) + (row0 + (GATED ? lane & 1 : 0)) * p.ld + f;
-    const bool mine = f < p.N;
+    const int64_t step = (GATED ? 2 : 1) * p.ld;
+    float y[GATED ? 16 : 32];
     if (GATED) {
         // lane 2i holds gate i, lane 2i + 1 up i: the even lane takes row j, the odd one row j + 1
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[j] : v[j + 1], 1);
-            const float g = (lane & 1) ? got : v[j], u = (lane & 1) ? v[j + 1] : got;
-            if (mine && j + (lane & 1) < rows) out[j * p.ld] = from_f32<T>(silu_fast(g) * u);
+        for (int j = 0; j < 16; ++j) {
+            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[2 * j] : v[2 * j + 1], 1);
+            const float g = (lane & 1) ? got : v[2 * j], u = (lane & 1) ? v[2 * j + 1] : got;
+            y[j] = silu_fast(g) * u;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (mine && j < rows) out[j * p.ld] = from_f32<T>(v[j]);
+        for (int j = 0; j < 32; ++j) y[j] = v[j];
+    }
+    constexpr int J = GATED ? 16 : 32;
+    if (rows == MX_CHUNK && f0 + (GATED ? 16 : 32) <= p.N) {   // a whole chunk: no predicates
+#pragma unroll
+        for (int j = 0; j < J; ++j, out += step) *out = from_f32<T>(y[j]);
+    } else if (f < p.N) {
+        const int mine = GATED ? (rows - (lane & 1) + 1) >> 1 : rows;
+#pragma unroll
+        for (int j = 0; j < J; ++j, out += step)
+            if (j < mine) *out = from_f32<T>(y[j]);
     }
 }
 
 // The same for MXFP4 output.  Gated, a pair of warps holds the 32 outputs of a block, 16 each
-// (half: which): they exchange their largest magnitudes and put their codes into one buffer,
+// (half: which): they exchange their scale bytes and put their codes into one buffer,
 // at two barriers of the pair; otherwise a warp holds a whole block and uses a buffer alone.
 template <bool GATED>
 __device__ __forceinline__ void mx_store_chunk_mxfp4(const MxArgs &p, const float (&v)[32], size_t row0, int rows, int f0,
                                                      uint8_t *buf, int bar, int half) {
     const int lane = threadIdx.x & 31;
     uint8_t *codes = buf;                                        // [32 rows][16]
-    uint32_t *amaxs = reinterpret_cast<uint32_t *>(buf + 512);   // [2][32 rows]
+    uint8_t *sc = buf + 512;                                     // [2][32 rows]
     if (GATED) {
         float h[16];
         uint32_t m[16];
@@ -174,12 +208,12 @@ __device__ __forceinline__ void mx_store_chunk_mxfp4(const MxArgs &p, const floa
             for (int j = 0; j < 16; ++j) m[j] = max(m[j], __shfl_xor_sync(0xffffffffu, m[j], o));
         if (lane < 2)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) amaxs[half * 32 + 2 * j + lane] = m[j];
+            for (int j = 0; j < 16; ++j) sc[half * 32 + 2 * j + lane] = (uint8_t)mx_scale_byte(m[j]);
         asm volatile("barrier.cta.sync %0, 64;" ::"r"(bar) : "memory");
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             const int r = 2 * j + (lane & 1);
-            const uint32_t s = mx_scale_byte(max(m[j], amaxs[(half ^ 1) * 32 + r]));
+            const uint32_t s = max(mx_scale_byte(m[j]), (uint32_t)sc[(half ^ 1) * 32 + r]);   // monotonic in the magnitude
             const float y = s == 255u ? 6.0f : h[j] * mx_inverse(s);
             const float next = __shfl_xor_sync(0xffffffffu, y, 2);
             if ((lane & 2) == 0) codes[r * 16 + half * 8 + (lane >> 2)] = (uint8_t)e2m1x2_code(y, next);
@@ -190,7 +224,7 @@ __device__ __forceinline__ void mx_store_chunk_mxfp4(const MxArgs &p, const floa
                 *reinterpret_cast<const uint4 *>(codes + lane * 16);
         } else if (half == 1 && lane < rows && f0 - 16 < p.N) {
             p.out_scales[(row0 + lane) * (p.N / MX_BLOCK) + (f0 - 16) / MX_BLOCK] =
-                (uint8_t)mx_scale_byte(max(amaxs[lane], amaxs[32 + lane]));
+                max(sc[lane], sc[32 + lane]);
         }
     } else {
         uint32_t my_scale = 0;
@@ -213,12 +247,14 @@ __device__ __forceinline__ void mx_store_chunk_mxfp4(const MxArgs &p, const floa
 }
 
 template <class C>
-__global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __grid_constant__ CUtensorMap tm_a, MxArgs p) {
+__global__ void __launch_bounds__(MX_THREADS, 1)
+    mxfp4_product_kernel(const __grid_constant__ CUtensorMap tm_nt, const __grid_constant__ CUtensorMap tm_box0,
+                         const __grid_constant__ CUtensorMap tm_box1, const __grid_constant__ MxArgs p) {
     extern __shared__ __align__(1024) uint8_t mx_smem_raw[];
     uint8_t *stages = mx_smem_raw + ((1024u - (smem_u32(mx_smem_raw) & 1023u)) & 1023u);
     uint8_t *epi = stages + C::STAGES * C::STAGE_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(epi + C::EPI_BYTES);
-    uint64_t *full = bars;                       // [S] producer (with the bytes) and the scale warp
+    uint64_t *full = bars;                       // [S] two producers (with their bytes) and the scale warp
     uint64_t *empty = full + C::STAGES;          // [S] MMA commit
     uint64_t *acc_full = empty + C::STAGES;      // [2] MMA commit
     uint64_t *acc_empty = acc_full + 2;          // [2] 4 epilogue warps
@@ -226,13 +262,12 @@ __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __gr
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(drain + 2);
     int *part = reinterpret_cast<int *>(drain + 3);          // [8]
-    int *S = reinterpret_cast<int *>(bars + 64);
-    static_assert((2 * C::STAGES + 8) * 8 + 32 <= 512, "barrier area");
+    int *S = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + C::BAR_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(smem_u32(full + s), 2);
+            mbar_init(smem_u32(full + s), 3);
             mbar_init(smem_u32(empty + s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -252,6 +287,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __gr
         int first, last;
         mx_group(p, e, first, last);
         S[e] = (last - first + C::NT - 1) / C::NT;
+        S[SR_MAX_EXPERTS + 1 + e] = first;
+        S[2 * (SR_MAX_EXPERTS + 1) + e] = last;
     }
     tc_fence_before();
     __syncthreads();
@@ -263,38 +300,42 @@ __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __gr
 
     const int packed_rows = C::GATED ? 2 * p.N : p.N;
     const int MT = (packed_rows + MX_TM - 1) / MX_TM, KT = (p.K + MX_TK - 1) / MX_TK;
-    const int64_t tiles = (int64_t)units * MT;
+    const uint32_t tiles = (uint32_t)units * MT;
+    MxTiles<C::NT> walk(S, p.E, MT, tiles);
 
-    if (warp == 0) {
-        // ------------------------------------------------------------------- producer
+    if (warp == 0 || warp == 3) {
+        // ---------------------------------------------------- producers: weights, row codes
+        // Issuing one TMA load takes about 100 cycles after 150 for the wait, so each producer
+        // has one load a step: one box holds all of a tile's rows.
+        const bool weights = warp == 0;
         uint32_t it = 0;
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-            const MxTile x = mx_tile(p, S, t, MT, C::NT);
+        for (; walk.more() && ok; walk.next()) {
+            const MxTile x = walk.get();
             const uint8_t *w = p.w + (size_t)x.e * p.expert_bytes + (size_t)x.m * KT * MX_TILE_BYTES;
-            const int boxes = (x.n + C::BOX - 1) / C::BOX;
+            const CUtensorMap *map = x.n <= C::BOX1 ? &tm_box1 : x.n <= C::BOX0 ? &tm_box0 : &tm_nt;
+            const uint32_t bytes = weights ? MX_TILE_BYTES : 128 * (x.n <= C::BOX1 ? C::BOX1 : x.n <= C::BOX0 ? C::BOX0 : C::NT);
             for (int kt = 0; kt < KT; ++kt, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (!(ok = mbar_wait(smem_u32(empty + s), ((it / C::STAGES) & 1) ^ 1, abort, p.status))) break;
                 if (elect_one()) {
                     const uint32_t st = smem_u32(stages + s * C::STAGE_BYTES), bar = smem_u32(full + s);
-                    mbar_expect_tx(bar, (uint32_t)(MX_TILE_BYTES + boxes * C::BOX * 128));
-                    bulk_g2s(st, w + (size_t)kt * MX_TILE_BYTES, MX_TILE_BYTES, bar);
-                    for (int j = 0; j < boxes; ++j)
-                        tma_load_2d(st + C::B_OFF + j * C::BOX * 128, &tm_a, kt * (MX_TK / 2), x.row0 + j * C::BOX, bar);
+                    mbar_expect_tx(bar, bytes);
+                    if (weights) bulk_g2s(st, w + (size_t)kt * MX_TILE_BYTES, MX_TILE_BYTES, bar);
+                    else tma_load_2d(st + C::B_OFF, map, kt * (MX_TK / 2), x.row0, bar);
                 }
                 __syncwarp();
             }
         }
-        if (!ok)   // no copy of this CTA may still be writing shared memory (a stage also waits for the scale warp)
+        if (!ok)   // no copy of this CTA may still be writing shared memory (a stage also waits for the other roles)
             for (uint32_t i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
                 mbar_drain(smem_u32(full + i % C::STAGES), (i / C::STAGES) & 1, p.status);
     } else if (warp == 1) {
         // ------------------------------------------------------------------------ MMA
         uint32_t it = 0, tc = 0;
         bool ok = true;
-        for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++tc) {
-            const MxTile x = mx_tile(p, S, t, MT, C::NT);
+        for (; walk.more() && ok; walk.next(), ++tc) {
+            const MxTile x = walk.get();
             const uint32_t b = tc & 1;
             if (!(ok = mbar_wait(smem_u32(acc_empty + b), ((tc >> 1) & 1) ^ 1, abort, p.status))) break;
             tc_fence_after();
@@ -353,8 +394,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __gr
                     for (uint32_t i = it - pending; i < it - pending + n; ++i) mbar_arrive(smem_u32(full + i % C::STAGES));
                 pending -= n;
             };
-            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const MxTile x = mx_tile(p, S, t, MT, C::NT);
+            for (; walk.more() && ok; walk.next()) {
+                const MxTile x = walk.get();
                 const uint8_t *src = p.a_scales + (size_t)(x.row0 + lane) * kb;
                 for (int kt = 0; kt < KT; ++kt) {
                     const uint32_t s = it % C::STAGES, bar = smem_u32(empty + s), parity = ((it / C::STAGES) & 1) ^ 1;
@@ -387,8 +428,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __gr
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             publish(pending);
         } else {
-            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const MxTile x = mx_tile(p, S, t, MT, C::NT);
+            for (; walk.more() && ok; walk.next()) {
+                const MxTile x = walk.get();
                 for (int kt = 0; kt < KT; ++kt, ++it) {
                     const uint32_t s = it % C::STAGES;
                     if (!(ok = mbar_wait(smem_u32(empty + s), ((it / C::STAGES) & 1) ^ 1, abort, p.status))) break;
@@ -410,8 +451,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1) mxfp4_product_kernel(const __gr
         uint8_t *pair_buf = epi + pair * MX_PAIR_BYTES;
         const int bar = 1 + pair;
         uint32_t tc = 0, used = 0;
-        for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
-            const MxTile x = mx_tile(p, S, t, MT, C::NT);
+        for (; walk.more(); walk.next(), ++tc) {
+            const MxTile x = walk.get();
             const uint32_t b = tc & 1;
             // the two warps of a pair leave together: they meet at barriers in their chunks
             uint32_t ok = mbar_wait(smem_u32(acc_full + b), (tc >> 1) & 1, abort, p.status, nullptr, 0, 0, 64);

@@ -119,19 +119,23 @@ bool row_map(CUtensorMap *m, const void *codes, int rows, int K, int box_rows) {
 
 template <class C>
 ds4moe_status run_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
-    CUtensorMap tm{};
-    if (!row_map(&tm, a.a_codes, a.rows, a.K, C::BOX)) return fail(h, DS4MOE_ECUDA, "tensor map of the rows");
+    const int64_t row_tiles = a.rows / C::NT + a.E, m_tiles = ((int64_t)a.N * (a.gated ? 2 : 1) + MX_TM - 1) / MX_TM;
+    if (row_tiles * m_tiles + h->num_sms > INT32_MAX) return fail(h, DS4MOE_EINVAL, "too many tiles for one call");
+    CUtensorMap tm[3];
+    const int boxes[3] = {C::NT, C::BOX0, C::BOX1};
+    for (int i = 0; i < 3; ++i)
+        if (!row_map(&tm[i], a.a_codes, a.rows, a.K, boxes[i])) return fail(h, DS4MOE_ECUDA, "tensor map of the rows");
     CK(h, cudaFuncSetAttribute(mxfp4_product_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM));
-    mxfp4_product_kernel<C><<<h->num_sms, MX_THREADS, C::SMEM, st>>>(tm, a);
+    mxfp4_product_kernel<C><<<h->num_sms, MX_THREADS, C::SMEM, st>>>(tm[0], tm[1], tm[2], a);
     CK(h, cudaGetLastError());
     return DS4MOE_OK;
 }
 template <bool GATED>
 ds4moe_status pick_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
     const double per_expert = (double)a.rows / std::min(a.rows, a.E);
-    if (per_expert <= 24) return run_product<MxCfg<32, 8, 8, GATED>>(h, a, st);
-    if (per_expert <= 112) return run_product<MxCfg<128, 32, 5, GATED>>(h, a, st);
-    return run_product<MxCfg<192, 32, 5, GATED>>(h, a, st);
+    if (per_expert <= 24) return run_product<MxCfg<32, 16, 8, 8, GATED>>(h, a, st);
+    if (per_expert <= 112) return run_product<MxCfg<128, 64, 32, 5, GATED>>(h, a, st);
+    return run_product<MxCfg<192, 128, 64, 5, GATED>>(h, a, st);
 }
 
 }  // namespace
