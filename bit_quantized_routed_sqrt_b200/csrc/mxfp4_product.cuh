@@ -38,7 +38,7 @@ __device__ __forceinline__ void mx_group(const MxArgs &p, int e, int &first, int
 //   warp 1     allocates tensor memory; copies the step's scales there (tcgen05.cp) and issues
 //              the MMAs.  Every stage has its own scale columns, so a copy never meets an MMA
 //              that still reads the columns' last contents
-//   warp 2     rows' scales (rows start anywhere, K / 32 is any number), laid out in shared
+//   warps 2,12 rows' scales (rows start anywhere, K / 32 is any number), laid out in shared
 //              memory as the copy wants them
 //   warps 4-11 epilogue, in two groups of four that take chunks of 32 rows in turn: accumulators
 //              -> silu(g) * u -> output.  A lane is an output, so a warp stores 32 (gated: two
@@ -48,8 +48,7 @@ __device__ __forceinline__ void mx_group(const MxArgs &p, int e, int &first, int
 // The accumulators are double buffered, so a tile's epilogue overlaps the next tile.
 // Every wait is bounded, as in the layer's grouped GEMM: on a timeout the CTA records
 // ETIMEOUT, waits for its own copies and MMAs, frees tensor memory and returns.
-constexpr int MX_THREADS = 384;
-constexpr int MX_SF_AHEAD = 3;           // steps of row scales in flight
+constexpr int MX_THREADS = 416;
 constexpr int MX_CHUNK = 32;             // rows of a (accumulator columns) that an epilogue warp takes at a time
 // MXFP4 output: of each pair of epilogue warps, two buffers of the codes of 32 rows x 32
 // outputs and of each warp's scale bytes
@@ -75,7 +74,7 @@ struct MxCfg {
     static constexpr int S_BYTES = 3 * (SR_MAX_EXPERTS + 1) * 4;
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES + S_BYTES;
     static_assert(COLS <= 512, "tensor memory");
-    static_assert(STAGES > MX_SF_AHEAD, "scales in flight");
+    static_assert(STAGES >= 4, "a scale warp waits on every other pair of steps, at most 3 steps apart");
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
     static_assert(NT % 16 == 0 && NT > BOX0 && BOX0 > BOX1 && BOX1 % 8 == 0, "row tiles");
     static_assert((2 * STAGES + 5) * 8 + 16 + 32 <= BAR_BYTES, "barrier area");
@@ -375,74 +374,93 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         if (elect_one()) tc_commit(smem_u32(drain));
         __syncwarp();
         mbar_drain(smem_u32(drain), 0, p.status);
-    } else if (warp == 2) {
+    } else if (warp == 2 || warp == 12) {
         // ----------------------------------------------------------------- row scales
         // Chunk (g, c) of a stage: 16 bytes for each l < 32, the four bytes of rows
-        // 128 c + 32 j + l, j < 4.  Words come by asynchronous copies (zeros for rows that are
-        // not the tile's), up to MX_SF_AHEAD steps in flight: with one step of register
-        // prefetch every K step took an L2 round trip (1.13 ms against XXX at 65536 rows x
-        // 7168 x 2048).  K / 32 not a multiple of four leaves words unaligned: bytes then.
-        const int kb = p.K / MX_BLOCK;
-        uint32_t it = 0;
+        // 128 c + 32 j + l, j < 4.  A lane takes the 16 bytes of a row for two steps at once;
+        // the two warps take such pairs of steps in turn and load one ahead, so a pair's loads
+        // have four steps to arrive.  (4-byte asynchronous copies, one for each word of a step,
+        // took 1140 cycles a step at 192 rows: 32 lines each.)
+        constexpr int R = (C::NT + 31) / 32;
+        const uint32_t which = warp == 2 ? 0 : 1;
+        const int kb = p.K / MX_BLOCK, PT = (KT + 1) / 2;
+        const bool aligned = kb % 16 == 0 && ((uintptr_t)p.a_scales & 15) == 0;
+        uint32_t cur[R][4], nxt[R][4];
+        uint32_t it0 = 0;        // the tile's first step
+        uint32_t g = 0;          // pairs of steps before this one, all tiles
+        MxTile x{};
+        int pt = -1;             // the pair in nxt
+        uint32_t pt_it = 0;      // its first step
         bool ok = true;
-        if (kb % 4 == 0 && ((uintptr_t)p.a_scales & 3) == 0) {
-            uint32_t pending = 0;   // the last steps whose copies may be in flight
-            auto publish = [&](uint32_t n) {   // the n oldest of them have landed
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0)
-                    for (uint32_t i = it - pending; i < it - pending + n; ++i) mbar_arrive(smem_u32(full + i % C::STAGES));
-                pending -= n;
-            };
-            for (; walk.more() && ok; walk.next()) {
-                const MxTile x = walk.get();
-                const uint8_t *src = p.a_scales + (size_t)(x.row0 + lane) * kb;
-                for (int kt = 0; kt < KT; ++kt) {
-                    const uint32_t s = it % C::STAGES, bar = smem_u32(empty + s), parity = ((it / C::STAGES) & 1) ^ 1;
-                    if (!__all_sync(0xffffffffu, mbar_try_spin(bar, parity))) {
-                        // no free stage: hand over what there is meanwhile
-                        asm volatile("cp.async.wait_group 0;" ::: "memory");
-                        publish(pending);
-                        if (!(ok = mbar_wait(bar, parity, abort, p.status))) break;
-                    }
-                    const uint32_t dst = smem_u32(stages + s * C::STAGE_BYTES) + MX_TILE_BYTES + lane * 16;
+        auto load = [&](int pair) {
 #pragma unroll
-                    for (int j = 0; j < 4 * C::SF_CHUNKS; ++j) {
-                        if (32 * j >= C::NT) break;
+            for (int j = 0; j < R; ++j) {
+                if (32 * j >= x.n) break;
+                const uint8_t *src = p.a_scales + (size_t)(x.row0 + min(32 * j + lane, x.n - 1)) * kb + pair * 16;
+                if (aligned) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src));
+                    nxt[j][0] = u.x; nxt[j][1] = u.y; nxt[j][2] = u.z; nxt[j][3] = u.w;
+                } else {
+                    // aligned words that hold any of the row's bytes, shifted; bytes past K are 0
+                    const int left = kb - pair * 16;   // at least 1
+                    const uint32_t *word = reinterpret_cast<const uint32_t *>((uintptr_t)src & ~(uintptr_t)3);
+                    const int off = (int)((uintptr_t)src & 3);
+                    uint32_t v[5];
 #pragma unroll
-                        for (int g = 0; g < 2; ++g)
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                                             dst + 512 * (g * C::SF_CHUNKS + j / 4) + 4 * (j & 3)),
-                                         "l"(32 * j + lane < x.n && kt * 8 + 4 * g < kb ? src + (size_t)32 * j * kb + kt * 8 + 4 * g : p.a_scales),
-                                         "r"(32 * j + lane < x.n && kt * 8 + 4 * g < kb ? 4 : 0)
-                                         : "memory");
-                    }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    ++it;
-                    if (++pending > MX_SF_AHEAD) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(MX_SF_AHEAD) : "memory");
-                        publish(1);
+                    for (int i = 0; i < 5; ++i) v[i] = 4 * i < off + min(left, 16) ? __ldg(word + i) : 0u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int valid = left - 4 * i;
+                        nxt[j][i] = __funnelshift_r(v[i], v[i + 1], 8 * off) &
+                                    (valid >= 4 ? 0xffffffffu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u);
                     }
                 }
             }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            publish(pending);
-        } else {
-            for (; walk.more() && ok; walk.next()) {
-                const MxTile x = walk.get();
-                for (int kt = 0; kt < KT; ++kt, ++it) {
-                    const uint32_t s = it % C::STAGES;
-                    if (!(ok = mbar_wait(smem_u32(empty + s), ((it / C::STAGES) & 1) ^ 1, abort, p.status))) break;
-                    uint8_t *dst = stages + s * C::STAGE_BYTES + MX_TILE_BYTES;
-                    for (int i = lane; i < 8 * x.n; i += 32) {
-                        const int r = i >> 3, blk = i & 7;
-                        dst[512 * ((blk >> 2) * C::SF_CHUNKS + r / 128) + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (blk & 3)] =
-                            kt * 8 + blk < kb ? __ldg(p.a_scales + (size_t)(x.row0 + r) * kb + kt * 8 + blk) : 0;
+        };
+        // moves to this warp's next pair and loads it
+        auto advance = [&]() {
+            while (walk.more()) {
+                if (pt < 0) x = walk.get();
+                for (++pt; pt < PT; ++pt, ++g)
+                    if ((g & 1) == which) {
+                        pt_it = it0 + 2 * pt;
+                        load(pt);
+                        ++g;
+                        return;
                     }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(full + s));
+                pt = -1;
+                it0 += KT;
+                walk.next();
+            }
+        };
+        advance();
+        while (walk.more() && ok) {
+            const int chunk_rows = x.n, steps = min(2, KT - 2 * pt);
+            const uint32_t it = pt_it;
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cur[j][i] = nxt[j][i];
+            advance();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (h >= steps) break;
+                const uint32_t s = (it + h) % C::STAGES;
+                if (!(ok = mbar_wait(smem_u32(empty + s), (((it + h) / C::STAGES) & 1) ^ 1, abort, p.status))) break;
+                const uint32_t dst = smem_u32(stages + s * C::STAGE_BYTES) + MX_TILE_BYTES + lane * 16;
+#pragma unroll
+                for (int c = 0; c < C::SF_CHUNKS; ++c) {
+                    if (128 * c >= chunk_rows) break;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        sts_v4(dst + 512 * (q * C::SF_CHUNKS + c),
+                               make_uint4(cur[4 * c][2 * h + q], 4 * c + 1 < R ? cur[4 * c + 1 < R ? 4 * c + 1 : 0][2 * h + q] : 0u,
+                                          4 * c + 2 < R ? cur[4 * c + 2 < R ? 4 * c + 2 : 0][2 * h + q] : 0u,
+                                          4 * c + 3 < R ? cur[4 * c + 3 < R ? 4 * c + 3 : 0][2 * h + q] : 0u));
                 }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(full + s));
             }
         }
     } else if (warp >= 4) {
