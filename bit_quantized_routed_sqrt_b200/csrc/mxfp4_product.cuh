@@ -77,7 +77,7 @@ struct MxCfg {
     static_assert(STAGES >= 4, "a scale warp waits on every other pair of steps, at most 3 steps apart");
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
     static_assert(NT % 16 == 0 && NT > BOX0 && BOX0 > BOX1 && BOX1 % 8 == 0, "row tiles");
-    static_assert((2 * STAGES + 5) * 8 + 16 + 32 <= BAR_BYTES, "barrier area");
+    static_assert((2 * STAGES + 5) * 8 + 16 + 32 + 4 * STAGES <= BAR_BYTES, "barrier area");
 };
 
 // Instruction descriptor of kind::mxf4: E2M1 A and B (K-major), E8M0 scales, fp32 D, M = 128, N;
@@ -98,6 +98,20 @@ __device__ __forceinline__ void mx_copy_scales(uint32_t tmem, uint32_t smem) {
     // no swizzle; 8-row groups of 16-byte rows 128 bytes apart
     const uint64_t d = (uint64_t)((smem & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+}
+
+// Flags beside the rows of a step's tile.
+constexpr uint32_t MX_FIRST = 1u << 30, MX_LAST = 1u << 31;
+
+// Whether the phase of that parity has completed, without waiting.
+__device__ __forceinline__ uint32_t mx_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done;
 }
 
 struct MxTile {
@@ -261,6 +275,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(drain + 2);
     int *part = reinterpret_cast<int *>(drain + 3);          // [8]
+    volatile uint32_t *meta = reinterpret_cast<volatile uint32_t *>(part + 8);   // [S] rows | MX_FIRST | MX_LAST
     int *S = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + C::BAR_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -319,7 +334,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
                 if (!(ok = mbar_wait(smem_u32(empty + s), ((it / C::STAGES) & 1) ^ 1, abort, p.status))) break;
                 if (elect_one()) {
                     const uint32_t st = smem_u32(stages + s * C::STAGE_BYTES), bar = smem_u32(full + s);
-                    mbar_expect_tx(bar, bytes);
+                    if (!weights) meta[s] = x.n | (kt == 0 ? MX_FIRST : 0u) | (kt == KT - 1 ? MX_LAST : 0u);
+                    mbar_expect_tx(bar, bytes);   // releases meta to the MMA warp
                     if (weights) bulk_g2s(st, w + (size_t)kt * MX_TILE_BYTES, MX_TILE_BYTES, bar);
                     else tma_load_2d(st + C::B_OFF, map, kt * (MX_TK / 2), x.row0, bar);
                 }
@@ -331,45 +347,51 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
                 mbar_drain(smem_u32(full + i % C::STAGES), (i / C::STAGES) & 1, p.status);
     } else if (warp == 1) {
         // ------------------------------------------------------------------------ MMA
-        uint32_t it = 0, tc = 0;
-        bool ok = true;
-        for (; walk.more() && ok; walk.next(), ++tc) {
-            const MxTile x = walk.get();
-            const uint32_t b = tc & 1;
-            if (!(ok = mbar_wait(smem_u32(acc_empty + b), ((tc >> 1) & 1) ^ 1, abort, p.status))) break;
-            tc_fence_after();
-            const int N = (x.n + 15) & ~15;
-            const uint32_t idesc0 = mxf4_idesc(N, 0), idesc2 = mxf4_idesc(N, 2);
-            const uint32_t d = tmem + b * C::NT;
-            for (int kt = 0; kt < KT; ++kt, ++it) {
-                const uint32_t s = it % C::STAGES;
-                if (!(ok = mbar_wait(smem_u32(full + s), (it / C::STAGES) & 1, abort, p.status))) break;
-                tc_fence_after();
-                const uint32_t st = smem_u32(stages + s * C::STAGE_BYTES);
-                const uint32_t sfa = tmem + 2 * C::NT + s * C::SF_COLS, sfb = sfa + 8;
-                const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + C::B_OFF);
-                if (elect_one()) {
-                    // Unrolled, with every operand a constant off the step's base: a loop with
-                    // run-time bounds moved each instruction's operands to uniform registers
-                    // one by one and took 1000 cycles a step where the MMAs take 260 to 510.
-                    // Inputs past K are zeros, so the last step runs whole as well.
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        mx_copy_scales(sfa + 4 * g, st + MX_CODE_BYTES + 512 * g);
-#pragma unroll
-                        for (int c = 0; c < C::SF_CHUNKS; ++c)
-                            mx_copy_scales(sfb + 4 * (g * C::SF_CHUNKS + c), st + MX_TILE_BYTES + 512 * (g * C::SF_CHUNKS + c));
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mx_mma(d, ad + 2 * kk, bd + 2 * kk, kk & 1 ? idesc2 : idesc0, sfa + 4 * (kk >> 1),
-                               sfb + 4 * C::SF_CHUNKS * (kk >> 1), (kt | kk) != 0);
-                    tc_commit(smem_u32(empty + s));
-                }
-                __syncwarp();
+        // A step's rows and whether it begins or ends a tile come with its stage (meta), and
+        // the next stage's barrier is asked before this step's MMAs are issued, so that this
+        // warp, the one that bounds a step, neither walks the tiles (700 cycles each) nor waits
+        // out the 150 cycles of a successful barrier test.
+        const uint32_t mine = walk.more() ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0, total = mine * (uint32_t)KT;
+        uint32_t tc = 0, idesc0 = 0, idesc2 = 0, d = tmem, b = 0;
+        bool ok = true, ready = false;
+        for (uint32_t it = 0; it < total; ++it) {
+            const uint32_t s = it % C::STAGES;
+            if (!ready && !(ok = mbar_wait(smem_u32(full + s), (it / C::STAGES) & 1, abort, p.status))) break;
+            const uint32_t m = lds_u32(smem_u32(const_cast<const uint32_t *>(meta + s)));
+            if (m & MX_FIRST) {
+                b = tc & 1;
+                if (!(ok = mbar_wait(smem_u32(acc_empty + b), ((tc >> 1) & 1) ^ 1, abort, p.status))) break;
+                const int N = ((int)(m & 0xffffu) + 15) & ~15;
+                idesc0 = mxf4_idesc(N, 0);
+                idesc2 = mxf4_idesc(N, 2);
+                d = tmem + b * C::NT;
             }
-            if (ok && elect_one()) tc_commit(smem_u32(acc_full + b));
-            __syncwarp();
+            const uint32_t asked = mx_test(smem_u32(full + (it + 1) % C::STAGES), ((it + 1) / C::STAGES) & 1);
+            tc_fence_after();
+            const uint32_t st = smem_u32(stages + s * C::STAGE_BYTES);
+            const uint32_t sfa = tmem + 2 * C::NT + s * C::SF_COLS, sfb = sfa + 8;
+            const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + C::B_OFF);
+            if (elect_one()) {
+                // Unrolled, with every operand a constant off the step's base: a loop with
+                // run-time bounds moved each instruction's operands to uniform registers
+                // one by one and took 1000 cycles a step where the MMAs take 160 to 510.
+                // Inputs past K are zeros, so the last step runs whole as well.
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    mx_copy_scales(sfa + 4 * g, st + MX_CODE_BYTES + 512 * g);
+#pragma unroll
+                    for (int c = 0; c < C::SF_CHUNKS; ++c)
+                        mx_copy_scales(sfb + 4 * (g * C::SF_CHUNKS + c), st + MX_TILE_BYTES + 512 * (g * C::SF_CHUNKS + c));
+                }
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mx_mma(d, ad + 2 * kk, bd + 2 * kk, kk & 1 ? idesc2 : idesc0, sfa + 4 * (kk >> 1),
+                           sfb + 4 * C::SF_CHUNKS * (kk >> 1), kk != 0 || !(m & MX_FIRST));
+                tc_commit(smem_u32(empty + s));
+                if (m & MX_LAST) tc_commit(smem_u32(acc_full + b));
+            }
+            if (m & MX_LAST) ++tc;
+            ready = __all_sync(0xffffffffu, asked);
         }
         if (elect_one()) tc_commit(smem_u32(drain));
         __syncwarp();
