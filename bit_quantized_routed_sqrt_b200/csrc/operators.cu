@@ -87,12 +87,11 @@ bool router_ok(const ds4moe_router *r) {
            r->group_score >= DS4MOE_GROUP_MAX && r->group_score <= DS4MOE_GROUP_TOP2 &&
            (r->renormalise == 0 || r->renormalise == 1) && r->scale - r->scale == 0.0f;
 }
-// Tokens a block: 64, or 256 once the counts of 64-token blocks would be a long column to add up.
-int route_block(int T) { return T <= 16384 ? 64 : 256; }
+int route_blocks(int T) { return (int)(((int64_t)T + SR_BLOCK - 1) / SR_BLOCK); }
+// Counts and masks of every block, and the totals.
 size_t route_workspace(const ds4moe_router *r, int T) {
-    const int TB = route_block(T);
-    const size_t NB = ((size_t)T + TB - 1) / TB;
-    return NB <= 1 ? 0 : NB * r->n_experts * (4 + TB / 8);
+    const size_t NB = route_blocks(T);
+    return NB <= 1 ? 0 : (NB * (1 + SR_WORDS) + 1) * r->n_experts * 4;
 }
 
 // ------------------------------------------------------------------ MXFP4 products
@@ -167,29 +166,37 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
     a.E = r->n_experts; a.k = r->top_k; a.score = r->score; a.G = r->n_groups; a.topk_groups = r->topk_groups;
     a.top2 = r->group_score == DS4MOE_GROUP_TOP2; a.renormalise = r->renormalise; a.scale = r->scale;
     a.logits = logits_dev; a.type = logits_type; a.ld = ld;
-    a.T = T; a.TB = route_block(T); a.NB = (int)(((int64_t)T + a.TB - 1) / a.TB);
+    a.T = T; a.NB = route_blocks(T);
     a.bias = bias_dev;
     a.topk_idx = topk_idx_dev; a.topk_w = topk_w_dev;
     a.offsets = expert_offsets_dev; a.sorted_token = sorted_token_dev; a.sorted_slot = sorted_slot_dev; a.inv_pos = inv_pos_dev;
     if (permute && a.NB > 1) {
         if (!workspace_dev || (uintptr_t)workspace_dev % 4 || workspace_bytes < route_workspace(r, T)) return DS4MOE_EINVAL;
         a.cnt = static_cast<int *>(workspace_dev);
-        a.mask = reinterpret_cast<uint32_t *>(a.cnt + (size_t)a.NB * a.E);
+        a.total = a.cnt + (size_t)a.NB * a.E;
+        a.mask = reinterpret_cast<uint32_t *>(a.total + a.E);
     }
-    const size_t smem = (a.G > 1 ? (size_t)SR_WARPS * a.E * 8 : 0) + (size_t)a.E * (a.TB / 8 + 4);
-    static_assert(SR_WARPS * SR_MAX_EXPERTS * 8 + SR_MAX_EXPERTS * (256 / 8 + 4) <= 227 * 1024, "shared memory per CTA");
-    auto launch = [&](auto kernel) {
+    // one block: enough warps for its tokens
+    const int warps = a.NB > 1 ? SR_WARPS : std::min(std::max(T, SR_WARPS), SR_MAX_WARPS);
+    auto launch = [&](auto kernel, int npl) {
+        const size_t smem = (a.G > 1 ? (size_t)warps * 32 * npl * 8 : 0) + (size_t)a.E * (SR_WORDS + 1) * 4;
         if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        kernel<<<a.NB, 32 * SR_WARPS, smem, st>>>(a);
+        kernel<<<a.NB, 32 * warps, smem, st>>>(a);
     };
-    if (a.E <= 32) launch(scored_topk_kernel<1>);
-    else if (a.E <= 64) launch(scored_topk_kernel<2>);
-    else if (a.E <= 128) launch(scored_topk_kernel<4>);
-    else if (a.E <= 256) launch(scored_topk_kernel<8>);
-    else launch(scored_topk_kernel<16>);
+    static_assert(SR_MAX_WARPS * SR_MAX_EXPERTS * 8 + SR_MAX_EXPERTS * (SR_WORDS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
+    if (a.E <= 32) launch(scored_topk_kernel<1>, 1);
+    else if (a.E <= 64) launch(scored_topk_kernel<2>, 2);
+    else if (a.E <= 128) launch(scored_topk_kernel<4>, 4);
+    else if (a.E <= 256) launch(scored_topk_kernel<8>, 8);
+    else launch(scored_topk_kernel<16>, 16);
     ds4moe_status s = launched();
     if (s != DS4MOE_OK || !permute || a.NB == 1) return s;
-    scored_permute_kernel<<<a.NB, 32 * SR_WARPS, (size_t)a.E * 8, st>>>(a);
+    const int scanned = a.NB > SR_DIRECT;
+    if (scanned) {
+        scored_scan_kernel<<<(a.E + 7) / 8, 256, 0, st>>>(a);
+        if ((s = launched()) != DS4MOE_OK) return s;
+    }
+    scored_permute_kernel<<<a.NB, SCAN_THREADS, (size_t)a.E * (SR_WORDS + 2) * 4, st>>>(a, scanned);
     return launched();
 }
 
