@@ -87,11 +87,17 @@ bool router_ok(const ds4moe_router *r) {
            r->group_score >= DS4MOE_GROUP_MAX && r->group_score <= DS4MOE_GROUP_TOP2 &&
            (r->renormalise == 0 || r->renormalise == 1) && r->scale - r->scale == 0.0f;
 }
-int route_blocks(int T) { return (int)(((int64_t)T + SR_BLOCK - 1) / SR_BLOCK); }
+// Tokens a block: about four blocks an SM where there are tokens for it.
+int route_block(int T) {
+    int TB = T <= 64 ? 64 : SR_MIN_BLOCK;
+    while (TB < SR_MAX_BLOCK && T / TB > 592) TB *= 2;
+    return TB;
+}
 // Counts and masks of every block, and the totals.
 size_t route_workspace(const ds4moe_router *r, int T) {
-    const size_t NB = route_blocks(T);
-    return NB <= 1 ? 0 : (NB * (1 + SR_WORDS) + 1) * r->n_experts * 4;
+    const int TB = route_block(T);
+    const size_t NB = ((size_t)T + TB - 1) / TB;
+    return NB <= 1 ? 0 : (NB * (1 + TB / 32) + 1) * r->n_experts * 4;
 }
 
 // ------------------------------------------------------------------ MXFP4 products
@@ -166,7 +172,7 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
     a.E = r->n_experts; a.k = r->top_k; a.score = r->score; a.G = r->n_groups; a.topk_groups = r->topk_groups;
     a.top2 = r->group_score == DS4MOE_GROUP_TOP2; a.renormalise = r->renormalise; a.scale = r->scale;
     a.logits = logits_dev; a.type = logits_type; a.ld = ld;
-    a.T = T; a.NB = route_blocks(T);
+    a.T = T; a.TB = route_block(T); a.NB = (int)(((int64_t)T + a.TB - 1) / a.TB);
     a.bias = bias_dev;
     a.topk_idx = topk_idx_dev; a.topk_w = topk_w_dev;
     a.offsets = expert_offsets_dev; a.sorted_token = sorted_token_dev; a.sorted_slot = sorted_slot_dev; a.inv_pos = inv_pos_dev;
@@ -178,25 +184,38 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
     }
     // one block: enough warps for its tokens
     const int warps = a.NB > 1 ? SR_WARPS : std::min(std::max(T, SR_WARPS), SR_MAX_WARPS);
-    auto launch = [&](auto kernel, int npl) {
-        const size_t smem = (a.G > 1 ? (size_t)warps * 32 * npl * 8 : 0) + (size_t)a.E * (SR_WORDS + 1) * 4;
+    auto launch = [&](auto many, auto lone, int npl) {
+        auto kernel = a.NB > 1 ? many : lone;
+        const size_t smem = (a.G > 1 ? (size_t)warps * 32 * npl * 8 : 0) + (size_t)a.E * (a.TB / 32 + 1) * 4;
         if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         kernel<<<a.NB, 32 * warps, smem, st>>>(a);
     };
-    static_assert(SR_MAX_WARPS * SR_MAX_EXPERTS * 8 + SR_MAX_EXPERTS * (SR_WORDS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
-    if (a.E <= 32) launch(scored_topk_kernel<1>, 1);
-    else if (a.E <= 64) launch(scored_topk_kernel<2>, 2);
-    else if (a.E <= 128) launch(scored_topk_kernel<4>, 4);
-    else if (a.E <= 256) launch(scored_topk_kernel<8>, 8);
-    else launch(scored_topk_kernel<16>, 16);
+    static_assert(SR_MAX_WARPS * SR_MAX_EXPERTS * 8 + SR_MAX_EXPERTS * (SR_MAX_BLOCK / 32 + 1) * 4 <= 227 * 1024,
+                  "shared memory per CTA");
+    auto typed = [&](auto v) {
+        using E = decltype(v);
+        // a lane's logits as one aligned piece: the common counts of experts
+        const bool vec = (uintptr_t)logits_dev % 16 == 0 && ld * sizeof(E) % 16 == 0;
+        if (a.E <= 32) launch(scored_topk_kernel<1, E, false, false>, scored_topk_kernel<1, E, false, true>, 1);
+        else if (a.E <= 64) launch(scored_topk_kernel<2, E, false, false>, scored_topk_kernel<2, E, false, true>, 2);
+        else if (a.E == 128 && vec) launch(scored_topk_kernel<4, E, true, false>, scored_topk_kernel<4, E, true, true>, 4);
+        else if (a.E <= 128) launch(scored_topk_kernel<4, E, false, false>, scored_topk_kernel<4, E, false, true>, 4);
+        else if (a.E == 256 && vec) launch(scored_topk_kernel<8, E, true, false>, scored_topk_kernel<8, E, true, true>, 8);
+        else if (a.E <= 256) launch(scored_topk_kernel<8, E, false, false>, scored_topk_kernel<8, E, false, true>, 8);
+        else if (a.E == 512 && vec) launch(scored_topk_kernel<16, E, true, false>, scored_topk_kernel<16, E, true, true>, 16);
+        else launch(scored_topk_kernel<16, E, false, false>, scored_topk_kernel<16, E, false, true>, 16);
+    };
+    if (logits_type == DS4MOE_F32) typed(float{});
+    else if (logits_type == DS4MOE_BF16) typed(__nv_bfloat16{});
+    else typed(__half{});
     ds4moe_status s = launched();
     if (s != DS4MOE_OK || !permute || a.NB == 1) return s;
     const int scanned = a.NB > SR_DIRECT;
     if (scanned) {
-        scored_scan_kernel<<<(a.E + 7) / 8, 256, 0, st>>>(a);
+        scored_scan_kernel<<<(a.E + 31) / 32, 1024, 0, st>>>(a);
         if ((s = launched()) != DS4MOE_OK) return s;
     }
-    scored_permute_kernel<<<a.NB, SCAN_THREADS, (size_t)a.E * (SR_WORDS + 2) * 4, st>>>(a, scanned);
+    scored_permute_kernel<<<a.NB, SCAN_THREADS, (size_t)a.E * (a.TB / 32 + 2) * 4, st>>>(a, scanned);
     return launched();
 }
 

@@ -8,9 +8,9 @@ namespace ds4 {
 
 constexpr int SR_MAX_TOPK = 32;
 constexpr int SR_MAX_GROUPS = 32;
-constexpr int SR_BLOCK = 64, SR_WORDS = SR_BLOCK / 32;   // tokens a CTA
+constexpr int SR_MIN_BLOCK = 32, SR_MAX_BLOCK = 256;     // tokens a CTA
 constexpr int SR_WARPS = 8, SR_MAX_WARPS = 16;           // warps a CTA (a lone CTA: up to 16)
-constexpr int SR_DIRECT = 64;                            // blocks whose counts every CTA adds up itself
+constexpr int SR_DIRECT = 128;                           // blocks whose counts every CTA adds up itself
 
 enum : int { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1, SCORE_SQRT_SOFTPLUS = 2 };
 
@@ -20,13 +20,13 @@ struct ScoredArgs {
     const void *logits;
     int type;
     int64_t ld;
-    int T, NB;               // tokens, blocks
+    int T, TB, NB;           // tokens, tokens a block (a power of two), blocks
     const float *bias;       // [E] or null
     int *topk_idx;           // [T][k]
     float *topk_w;
     int *offsets, *sorted_token, *sorted_slot, *inv_pos;   // each may be null
     int *cnt;                // workspace [NB][E]
-    uint32_t *mask;          // workspace [NB][E][SR_WORDS]
+    uint32_t *mask;          // workspace [NB][E][TB / 32]
     int *total;              // workspace [E]
 };
 
@@ -55,7 +55,7 @@ __device__ __forceinline__ void warp_best(double &v, int &i) {
 
 // The choice of one token in fp64, by one warp; lane holds experts lane + 32 i.  Returns to
 // lane j < k the expert of slot j (-1: no candidate was left).  About 3000 instructions a
-// token at 256 experts: it runs where scored_choice finds two values too close.
+// token at 256 experts: it runs where scored_choice and scored_rank cannot tell.
 template <int NPL>
 __device__ __noinline__ int scored_choice64(const ScoredArgs &p, int64_t t, double *scratch) {
     const int lane = threadIdx.x & 31;
@@ -144,9 +144,12 @@ __device__ __noinline__ int scored_choice64(const ScoredArgs &p, int64_t t, doub
 // expert with its tie rule.  Each lane sorts its keys (a network of integer minima and maxima);
 // a slot is then one warp maximum over the lanes' heads and a shift in the lane that had it.
 // The order is certain where neighbours (the first expert left out among them) differ by more
-// than 2 M and the cut; anything closer, exact ties of fp32 logits among it, is decided by
-// scored_choice64.  Without a bias the values are the logits themselves: M is 0, and for fp16
+// than 2 M and the cut; where some are closer, exact ties of fp32 logits among them, scored_rank
+// orders all that may be among the first k by their fp64 values, and scored_choice64 does the
+// whole token where groups are too close or the candidates too many.  Without a bias the values are the logits themselves: M is 0, and for fp16
 // and bf16 logits the cut drops nothing, so nothing is left to decide.
+
+constexpr uint32_t SR_LIVE = 0x00800000u;   // the lowest key of a finite value
 
 __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t u = __float_as_uint(v);
@@ -163,6 +166,11 @@ __device__ __forceinline__ float approx_rcp(float x) {
 __device__ __forceinline__ float approx_sqrt(float x) {
     float r;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float approx_exp(float x) {   // ex2.approx(x log2 e), below 2^-126 zero
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.442695041f));
     return r;
 }
 // log(1 + t), 0 <= t <= 1, as 2 atanh(z) = 2 (z + z^3/3 + ...), z = t / (2 + t) <= 1/3: the series
@@ -195,50 +203,136 @@ __device__ __forceinline__ void sort_network(uint32_t (&v)[N]) {
                     }
 }
 
-// The choice of one token by one warp: to lane j < k the expert of slot j, or -1.
-template <int NPL>
-__device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, double *scratch) {
+// A token's logits in one lane: experts lane * NPL + i where a lane's are one aligned piece of
+// the row (VEC: E = 32 NPL), otherwise lane + 32 i.
+template <int NPL, class T, bool VEC>
+struct LaneLogits {
+    static constexpr int BYTES = NPL * (int)sizeof(T);
+    static constexpr int WORDS = VEC ? (BYTES + 3) / 4 : 1;
+    uint32_t w[WORDS];
+    T v[VEC ? 1 : NPL];
+
+    __device__ __forceinline__ static int expert(int lane, int i) { return VEC ? lane * NPL + i : lane + 32 * i; }
+    __device__ __forceinline__ void load(const ScoredArgs &p, int64_t t) {
+        const int lane = threadIdx.x & 31;
+        const T *row = reinterpret_cast<const T *>(p.logits) + t * p.ld;
+        if constexpr (VEC) {
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(row) + lane * BYTES;
+            if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+                for (int i = 0; i < BYTES / 16; ++i) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+                    w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+                }
+            } else {
+                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
+                w[0] = u.x; w[1] = u.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                if (lane + 32 * i < p.E) v[i] = row[lane + 32 * i];
+        }
+    }
+    // NaN and -inf: no candidate, -inf; +inf counts as the largest finite value.
+    __device__ __forceinline__ float get(const ScoredArgs &p, int i) const {
+        float x;
+        if constexpr (VEC) {
+            if constexpr (sizeof(T) == 4) x = __uint_as_float(w[i]);
+            else {
+                const uint16_t h = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+                x = to_f32<T>(*reinterpret_cast<const T *>(&h));
+            }
+        } else {
+            x = (threadIdx.x & 31) + 32 * i < p.E ? to_f32<T>(v[i]) : -INFINITY;
+        }
+        return x > -INFINITY ? fminf(x, 3.402823466e38f) : -INFINITY;
+    }
+};
+
+// Lane j < n holds candidate e (or -1): to lane j < k the j-th best of them by the exact choice
+// values (fp64), ties to the lower expert.
+template <int NPL, class T, bool VEC>
+__device__ __noinline__ int scored_rank(const ScoredArgs &p, int64_t t, const LaneLogits<NPL, T, VEC> &logits, int e, int n) {
+    const int lane = threadIdx.x & 31;
+    const bool on = lane < n && e >= 0;
+    double l = on ? (double)fminf(to_f32<T>(reinterpret_cast<const T *>(p.logits)[t * p.ld + e]), 3.402823466e38f) : -INFINITY;
+    double v = l;
+    if (p.bias) {   // otherwise ranked by the logits
+        double m = 0.0, inv_sum = 0.0;
+        if (p.score == SCORE_SOFTMAX) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) top = fmaxf(top, logits.get(p, i));
+            m = (double)warp_max_f32(top);
+            double sum = 0.0;
+            for (int i = 0; i < NPL; ++i) sum += logits.get(p, i) > -INFINITY ? exp((double)logits.get(p, i) - m) : 0.0;
+            inv_sum = 1.0 / warp_sum(sum);
+        }
+        if (on) v = score64(p.score, l, m, inv_sum) + (double)p.bias[e];
+    }
+    int rank = 0;
+    for (int h = 0; h < n; ++h) {
+        const double ov = __shfl_sync(0xffffffffu, v, h);
+        const int oe = __shfl_sync(0xffffffffu, on ? e : -1, h);
+        rank += oe >= 0 && (ov > v || (ov == v && oe < e));
+    }
+    int got = -1;
+    for (int h = 0; h < n; ++h) {
+        const int r = __shfl_sync(0xffffffffu, on ? rank : -1, h), oe = __shfl_sync(0xffffffffu, e, h);
+        if (r == lane) got = oe;
+    }
+    return lane < p.k ? got : -1;
+}
+
+// The choice of one token by one warp: to lane j < k the expert of slot j, or -1.  bias: the
+// lane's experts' (if any).
+template <int NPL, class T, bool VEC>
+__device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, const LaneLogits<NPL, T, VEC> &logits,
+                                             const float (&bias)[NPL], double *scratch) {
+    using L = LaneLogits<NPL, T, VEC>;
     constexpr uint32_t LOW = NPL <= 8 ? 255u : 511u;   // room for the index
     const int lane = threadIdx.x & 31;
     const bool by_score = p.bias || (p.G > 1 && p.top2);
-    float l[NPL];
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < p.E ? load_typed(p.logits, p.type, t * p.ld + e) : -INFINITY;
-    }
     float a[NPL], M = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) a[i] = l[i] > -INFINITY ? fminf(l[i], 3.402823466e38f) : -INFINITY;   // NaN: out
+    for (int i = 0; i < NPL; ++i) a[i] = logits.get(p, i);
     if (by_score) {
-        // M: each score is off by at most (16 + |x|) 2^-22 of itself, x the exponential's
-        // argument (ex2.approx 2^-22, its argument's rounding 1.5 |x| 2^-24, reciprocal, root,
-        // series and sum less than 2^-21 together), the sum with the bias by 2^-24; below
-        // e^-87 the exponentials may be flushed to 0, a score (a root) of up to 1.3e-19.
-        float off = 0.0f, size = 0.0f, top = 0.0f, scale = 1.0f;
+        // M: each score is off by at most (4 + |x|) 2^-22 of itself, x the exponential's argument
+        // (ex2.approx 2^-22, its argument's rounding 1.5 |x| 2^-24, reciprocal and root 2^-23
+        // each, the series' roundings 2^-22; a root halves what comes before it), 4 more where a
+        // sum of 512 is in it (13 additions, its terms' errors, its reciprocal), and the sum with
+        // the bias is off by 2^-24; below e^-87 the exponentials may be flushed to 0, a score (a
+        // root) of up to 1.3e-19.
+        float off = 0.0f, size = 0.0f;
+        auto take = [&](int i, float s, float weight) {   // a score and (4 or 8 + |x|)
+            const bool live = a[i] > -INFINITY;
+            off = fmaxf(off, live ? s * weight : 0.0f);
+            if (p.bias) s += bias[i];
+            a[i] = live && s > -INFINITY ? s : -INFINITY;
+            size = fmaxf(size, live ? fabsf(s) : 0.0f);   // of a NaN: not taken
+        };
+        // (one loop for each score: a test inside the loop costs as much as a score)
         if (p.score == SCORE_SOFTMAX) {
-            top = -INFINITY;
+            float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < NPL; ++i) top = fmaxf(top, a[i]);
-            top = warp_max_f32(top);
-            float sum = 0.0f;
+            top = fmaxf(warp_max_f32(top), -3.402823466e38f);
+            float sum = 0.0f, e[NPL];
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) sum += a[i] > -INFINITY ? __expf(a[i] - top) : 0.0f;
-            scale = approx_rcp(warp_sum(sum));
-        }
+            for (int i = 0; i < NPL; ++i) sum += e[i] = approx_exp(a[i] - top);   // of -inf: 0
+            const float scale = approx_rcp(warp_sum(sum));
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            if (!(a[i] > -INFINITY)) continue;
-            const float x = p.score == SCORE_SOFTMAX ? a[i] - top : p.score == SCORE_SIGMOID ? -a[i] : -fabsf(a[i]);
-            const float ex = __expf(x);
-            float s;
-            if (p.score == SCORE_SOFTMAX) s = ex * scale;
-            else if (p.score == SCORE_SIGMOID) s = approx_rcp(1.0f + ex);
-            else s = approx_sqrt(fmaxf(a[i], 0.0f) + log1p_unit(ex, approx_rcp(2.0f + ex)));
-            off = fmaxf(off, s * (16.0f + fminf(fabsf(x), 1e4f)));
-            if (p.bias) s += p.bias[lane + 32 * i];
-            a[i] = s > -INFINITY ? s : -INFINITY;
-            size = fmaxf(size, fabsf(s));   // of a NaN: not taken
+            for (int i = 0; i < NPL; ++i) take(i, e[i] * scale, 8.0f - (a[i] - top));
+        } else if (p.score == SCORE_SIGMOID) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) take(i, approx_rcp(1.0f + approx_exp(-a[i])), 4.0f + fabsf(a[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const float ex = approx_exp(-fabsf(a[i]));
+                take(i, approx_sqrt(fmaxf(a[i], 0.0f) + log1p_unit(ex, approx_rcp(2.0f + ex))), 4.0f + fabsf(a[i]));
+            }
         }
         M = warp_max_f32(fmaf(off, 2.384185791e-7f, fmaf(size, 1.192092896e-7f, 2e-19f)));
     }
@@ -246,7 +340,7 @@ __device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, dou
     uint32_t key[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-        key[i] = a[i] > -INFINITY ? (order_key(a[i]) & ~LOW) | (LOW - (uint32_t)(lane + 32 * i)) : 0u;
+        key[i] = (order_key(a[i]) & ~LOW) | (LOW - (uint32_t)L::expert(lane, i));   // of -inf: below SR_LIVE
     if (p.G > 1) {
         // group values by lane, from the experts' values in shared memory (padded: no conflicts)
         const int per = p.E / p.G;
@@ -254,7 +348,7 @@ __device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, dou
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
-            if (lane + 32 * i < p.E) v[33 * i + lane] = a[i];
+            if (L::expert(lane, i) < p.E) v[L::expert(lane, i) + (L::expert(lane, i) >> 5)] = a[i];
         __syncwarp();
         float best = -INFINITY, next = -INFINITY;
         if (lane < p.G) {
@@ -282,34 +376,49 @@ __device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, dou
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             // (e + 1/2) / per is at least 1/2 / 512 from a whole number: the product's rounding cannot cross it
-            const int of = (int)(((float)(lane + 32 * i) + 0.5f) * inv);
-            if (!((kept >> of) & 1u)) key[i] = 0u;
-            else if (!p.bias && by_score && key[i])   // ranked by the logit, chosen groups by their scores
-                key[i] = (order_key(fminf(l[i], 3.402823466e38f)) & ~LOW) | (LOW - (uint32_t)(lane + 32 * i));
+            const int of = (int)(((float)L::expert(lane, i) + 0.5f) * inv);
+            if (!((kept >> (of & 31)) & 1u)) key[i] = 0u;
+            else if (!p.bias && by_score && key[i] >= SR_LIVE)   // ranked by the logit, chosen groups by their scores
+                key[i] = (order_key(logits.get(p, i)) & ~LOW) | (LOW - (uint32_t)L::expert(lane, i));
         }
         if (!p.bias) M = 0.0f;
     }
+    if (!sure) return scored_choice64<NPL>(p, t, scratch);
     sort_network<NPL>(key);
-    uint32_t mine = 0, last = 0;
-    for (int j = 0; j <= p.k; ++j) {
+    auto pop = [&]() {   // the best key left, taken out
         const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
-        if (j == p.k) { last = best; break; }
-        if (lane == j) mine = best;
         if (key[0] == best) {
 #pragma unroll
             for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1];
             key[NPL - 1] = 0u;
         }
+        return best;
+    };
+    uint32_t mine = 0, last = 0;
+    for (int j = 0; j < p.k; ++j) {
+        const uint32_t best = pop();
+        if (lane == j) mine = best;
     }
-    if (p.bias || p.type == DT_F32) {
+    if (p.bias || sizeof(T) == 4) {
+        last = __reduce_max_sync(0xffffffffu, key[0]);
         uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
         if (lane == p.k - 1) next = last;
         // the value is at least what its key's upper bits say, the next one below their successor
         const float low = order_value(mine & ~LOW), high = order_value((next & ~LOW) + LOW + 1u);
-        sure = __all_sync(0xffffffffu, lane >= p.k || next == 0u || low - high >= 2.0f * M) && sure;
+        if (!__all_sync(0xffffffffu, lane >= p.k || next < SR_LIVE || low - high >= 2.0f * M)) {
+            // Every expert that may be among the first k, one a lane, by its exact value.
+            const float least = __shfl_sync(0xffffffffu, low, p.k - 1);   // the k-th is not below this less M
+            int n = p.k;
+            for (; last >= SR_LIVE && !(least - order_value((last & ~LOW) + LOW + 1u) >= 2.0f * M); ++n) {
+                if (n == 32) return scored_choice64<NPL>(p, t, scratch);
+                if (lane == n) mine = last;
+                pop();
+                last = __reduce_max_sync(0xffffffffu, key[0]);
+            }
+            return scored_rank<NPL, T, VEC>(p, t, logits, mine >= SR_LIVE ? (int)(LOW - (mine & LOW)) : -1, n);
+        }
     }
-    if (!sure) return scored_choice64<NPL>(p, t, scratch);
-    return lane < p.k && mine ? (int)(LOW - (mine & LOW)) : -1;
+    return lane < p.k && mine >= SR_LIVE ? (int)(LOW - (mine & LOW)) : -1;
 }
 
 // x - y and what its rounding left.
@@ -328,27 +437,20 @@ __device__ __forceinline__ float exp_diff(float x, float y, float half) {   // e
 // Renormalised, scores count up to a factor common to the token, exp(-m) (sqrt-softplus:
 // exp(-m / 2)) with m the largest chosen logit (softmax) or that where it is negative and 0
 // elsewhere: tokens whose scores all underflow have weights too.
-template <int NPL>
-__device__ __forceinline__ float scored_weight(const ScoredArgs &p, int64_t t, int e) {
-    const int lane = threadIdx.x & 31;
+template <int NPL, class T, bool VEC>
+__device__ __forceinline__ float scored_weight(const ScoredArgs &p, int64_t t, const LaneLogits<NPL, T, VEC> &logits, int e) {
     const bool on = e >= 0;
-    const float l = on ? fminf(load_typed(p.logits, p.type, t * p.ld + e), 3.402823466e38f) : -INFINITY;
+    const float l = on ? fminf(to_f32<T>(reinterpret_cast<const T *>(p.logits)[t * p.ld + e]), 3.402823466e38f) : -INFINITY;
     float m = 0.0f;
     double sum = 0.0;
     if (p.score == SCORE_SOFTMAX && !p.renormalise) {
         // the denominator takes every expert
-        float v[NPL];
         m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int o = lane + 32 * i;
-            const float x = o < p.E ? load_typed(p.logits, p.type, t * p.ld + o) : -INFINITY;
-            v[i] = x > -INFINITY ? fminf(x, 3.402823466e38f) : -INFINITY;
-            m = fmaxf(m, v[i]);
-        }
+        for (int i = 0; i < NPL; ++i) m = fmaxf(m, logits.get(p, i));
         m = warp_max_f32(m);
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) sum += v[i] > -INFINITY ? (double)expf(v[i] - m) : 0.0;
+        for (int i = 0; i < NPL; ++i) sum += logits.get(p, i) > -INFINITY ? (double)expf(logits.get(p, i) - m) : 0.0;
         sum = warp_sum(sum);
     } else if (p.renormalise) {
         m = warp_max_f32(l);
@@ -360,12 +462,16 @@ __device__ __forceinline__ float scored_weight(const ScoredArgs &p, int64_t t, i
             w = exp_diff(l, m, 1.0f);
         } else {
             const float ex = expf(-fabsf(l));
-            if (p.score == SCORE_SIGMOID) w = (l >= 0.0f ? 1.0f : exp_diff(l, m, 1.0f)) / (1.0f + ex);
-            else if (l >= 0.0f) w = sqrtf(l + log1p_unit(ex, 1.0f / (2.0f + ex)));
-            else w = exp_diff(l, m, 0.5f) * (ex > 1e-30f ? sqrtf(log1p_unit(ex, 1.0f / (2.0f + ex)) / ex) : 1.0f);
+            if (p.score == SCORE_SIGMOID) {
+                w = __fdividef(l >= 0.0f ? 1.0f : exp_diff(l, m, 1.0f), 1.0f + ex);
+            } else {
+                const float lp = log1p_unit(ex, approx_rcp(2.0f + ex));
+                if (l >= 0.0f) w = approx_sqrt(l + lp);
+                else w = exp_diff(l, m, 0.5f) * (ex > 1e-30f ? approx_sqrt(__fdividef(lp, ex)) : 1.0f);
+            }
         }
     }
-    if (p.renormalise) w = w / warp_sum(w);
+    if (p.renormalise) w = __fdividef(w, warp_sum(w));
     else if (p.score == SCORE_SOFTMAX) w = (float)((double)w / sum);
     return on ? w * p.scale : 0.0f;
 }
@@ -380,7 +486,7 @@ __device__ __forceinline__ void scored_scatter(const ScoredArgs &p, int t0, int 
         int pos = -1;
         if (e >= 0) {
             pos = base[e];
-            const uint32_t *me = mask + e * SR_WORDS;
+            const uint32_t *me = mask + e * (p.TB / 32);
             for (int w = 0; w < tl / 32; ++w) pos += __popc(me[w]);
             pos += __popc(me[tl / 32] & ((1u << (tl & 31)) - 1u));
             if (p.sorted_token) p.sorted_token[pos] = t0 + tl;
@@ -390,41 +496,51 @@ __device__ __forceinline__ void scored_scatter(const ScoredArgs &p, int t0, int 
     }
 }
 
-// Top-k of SR_BLOCK tokens a block.  With one block the permutation follows at once; otherwise
-// the block leaves its counts and masks to the kernels below.
-template <int NPL>
-__global__ void __launch_bounds__(32 * SR_MAX_WARPS) scored_topk_kernel(const __grid_constant__ ScoredArgs p) {
+// Top-k of TB tokens a block.  With one block the permutation follows at once; otherwise the
+// block leaves its counts and masks to the kernels below.  The next token's logits are loaded
+// before the present one is chosen from.
+template <int NPL, class T, bool VEC, bool LONE>
+__global__ void __launch_bounds__(32 * (LONE ? SR_MAX_WARPS : SR_WARPS), LONE || NPL > 8 ? 1 : 3) scored_topk_kernel(const __grid_constant__ ScoredArgs p) {
     extern __shared__ __align__(16) uint8_t sr_smem[];
-    const int warps = blockDim.x >> 5;
+    const int warps = blockDim.x >> 5, W = p.TB / 32;
     double *scratch = reinterpret_cast<double *>(sr_smem);                       // [warps][32 NPL], groups only
-    uint32_t *mask = reinterpret_cast<uint32_t *>(scratch + (p.G > 1 ? warps * 32 * NPL : 0));   // [E][SR_WORDS]
-    int *base = reinterpret_cast<int *>(mask + p.E * SR_WORDS);                  // [E]
+    uint32_t *mask = reinterpret_cast<uint32_t *>(scratch + (p.G > 1 ? warps * 32 * NPL : 0));   // [E][W]
+    int *base = reinterpret_cast<int *>(mask + p.E * W);                         // [E]
     __shared__ int part[SCAN_THREADS / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = blockIdx.x * SR_BLOCK, nt = min(SR_BLOCK, p.T - t0);
-    for (int i = threadIdx.x; i < p.E * SR_WORDS; i += blockDim.x) mask[i] = 0;
+    const int t0 = blockIdx.x * p.TB, nt = min(p.TB, p.T - t0);
+    LaneLogits<NPL, T, VEC> now, next;
+    if (warp < nt) next.load(p, t0 + warp);
+    float bias[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = LaneLogits<NPL, T, VEC>::expert(lane, i);
+        bias[i] = p.bias && e < p.E ? p.bias[e] : 0.0f;
+    }
+    for (int i = threadIdx.x; i < p.E * W; i += blockDim.x) mask[i] = 0;
     __syncthreads();
     for (int tl = warp; tl < nt; tl += warps) {
-        const int e = scored_choice<NPL>(p, t0 + tl, scratch + (p.G > 1 ? warp * 32 * NPL : 0));
-        const float w = scored_weight<NPL>(p, t0 + tl, e);
+        now = next;
+        if (tl + warps < nt) next.load(p, t0 + tl + warps);
+        const int e = scored_choice<NPL, T, VEC>(p, t0 + tl, now, bias, scratch + (p.G > 1 ? warp * 32 * NPL : 0));
+        const float w = scored_weight<NPL, T, VEC>(p, t0 + tl, now, e);
         if (lane < p.k) {
             const size_t pair = (size_t)(t0 + tl) * p.k + lane;
             p.topk_idx[pair] = e;
             p.topk_w[pair] = w;
-            if (e >= 0) atomicOr(&mask[e * SR_WORDS + tl / 32], 1u << (tl & 31));
+            if (e >= 0) atomicOr(&mask[e * W + tl / 32], 1u << (tl & 31));
         }
     }
+    if (p.NB > 1 && !p.cnt) return;   // no permutation
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
         int n = 0;
-#pragma unroll
-        for (int w = 0; w < SR_WORDS; ++w) n += __popc(mask[e * SR_WORDS + w]);
+        for (int w = 0; w < W; ++w) n += __popc(mask[e * W + w]);
         base[e] = n;
-        if (p.NB > 1 && p.cnt) p.cnt[(size_t)blockIdx.x * p.E + e] = n;
+        if (p.NB > 1) p.cnt[(size_t)blockIdx.x * p.E + e] = n;
     }
     if (p.NB > 1) {
-        if (p.cnt)
-            for (int i = threadIdx.x; i < p.E * SR_WORDS; i += blockDim.x) p.mask[(size_t)blockIdx.x * p.E * SR_WORDS + i] = mask[i];
+        for (int i = threadIdx.x; i < p.E * W; i += blockDim.x) p.mask[(size_t)blockIdx.x * p.E * W + i] = mask[i];
         return;
     }
     __syncthreads();
@@ -436,54 +552,57 @@ __global__ void __launch_bounds__(32 * SR_MAX_WARPS) scored_topk_kernel(const __
     scored_scatter(p, t0, nt, base, mask);
 }
 
-// Counts of the blocks -> the counts before each block, in place, and the totals.  A warp per
-// expert, eight neighbours a CTA (they share the counts' 32-byte sectors), each lane a run of
-// up to 32 blocks at a time.
-__global__ void __launch_bounds__(256) scored_scan_kernel(const __grid_constant__ ScoredArgs p) {
-    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (e >= p.E) return;
+// Counts of the blocks -> the counts before each block, in place, and the totals.  A CTA has 32
+// experts, one a lane; its warps take runs of blocks.
+__global__ void __launch_bounds__(1024) scored_scan_kernel(const __grid_constant__ ScoredArgs p) {
+    __shared__ int sums[32][33];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
+    const bool on = e < p.E;
     int carry = 0;
-    for (int b0 = 0; b0 < p.NB; b0 += 1024) {
-        const int each = (min(p.NB - b0, 1024) + 31) / 32, first = b0 + lane * each;
-        int v[32], sum = 0;
+    for (int b0 = 0; b0 < p.NB; b0 += 512) {
+        const int each = (min(p.NB - b0, 512) + 31) / 32, first = b0 + warp * each;
+        int v[16], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = i < each && first + i < p.NB ? p.cnt[(size_t)(first + i) * p.E + e] : 0;
+        for (int i = 0; i < 16; ++i) v[i] = on && i < each && first + i < p.NB ? p.cnt[(size_t)(first + i) * p.E + e] : 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) sum += v[i];
-        int before = sum;
+        for (int i = 0; i < 16; ++i) sum += v[i];
+        sums[warp][lane] = sum;
+        __syncthreads();
+        int at = carry, all = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += u;
+        for (int w = 0; w < 32; ++w) {
+            const int n = sums[w][lane];
+            at += w < warp ? n : 0;
+            all += n;
         }
-        const int all = __shfl_sync(0xffffffffu, before, 31);
-        int at = carry + before - sum;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            if (i < each && first + i < p.NB) p.cnt[(size_t)(first + i) * p.E + e] = at;
+        for (int i = 0; i < 16; ++i) {
+            if (on && i < each && first + i < p.NB) p.cnt[(size_t)(first + i) * p.E + e] = at;
             at += v[i];
         }
         carry += all;
+        __syncthreads();
     }
-    if (lane == 0) p.total[e] = carry;
+    if (on && warp == 0) p.total[e] = carry;
 }
 
 // Offsets and the places of one block's pairs.  scanned: cnt and total are those of
 // scored_scan_kernel; otherwise cnt holds the blocks' own counts, which every CTA adds up.
 __global__ void __launch_bounds__(SCAN_THREADS) scored_permute_kernel(const __grid_constant__ ScoredArgs p, int scanned) {
     extern __shared__ __align__(16) uint8_t sr_smem[];
+    const int W = p.TB / 32;
     int *base = reinterpret_cast<int *>(sr_smem), *before = base + p.E;   // [E] each
-    uint32_t *mask = reinterpret_cast<uint32_t *>(before + p.E);          // [E][SR_WORDS]
+    uint32_t *mask = reinterpret_cast<uint32_t *>(before + p.E);          // [E][W]
     __shared__ int part[SCAN_THREADS / 32];
-    const int t0 = blockIdx.x * SR_BLOCK, nt = min(SR_BLOCK, p.T - t0);
-    for (int i = threadIdx.x; i < p.E * SR_WORDS; i += blockDim.x) mask[i] = p.mask[(size_t)blockIdx.x * p.E * SR_WORDS + i];
+    const int t0 = blockIdx.x * p.TB, nt = min(p.TB, p.T - t0);
+    for (int i = threadIdx.x; i < p.E * W; i += blockDim.x) mask[i] = p.mask[(size_t)blockIdx.x * p.E * W + i];
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
         if (scanned) {
             base[e] = p.total[e];
             before[e] = p.cnt[(size_t)blockIdx.x * p.E + e];
         } else {
             int all = 0, mine = 0;
-#pragma unroll 16
+#pragma unroll 32
             for (int b = 0; b < p.NB; ++b) {
                 const int n = p.cnt[(size_t)b * p.E + e];
                 mine += b < blockIdx.x ? n : 0;
