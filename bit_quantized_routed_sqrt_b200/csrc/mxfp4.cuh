@@ -50,15 +50,28 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// N consecutive values, N * sizeof(T) a multiple of 16 and p 16-byte aligned, or one by one.
+// 32 bytes at once (32-byte aligned): a lane's load is a whole sector.
+__device__ __forceinline__ void ld_stream_v8(const void *p, uint32_t (&r)[8]) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void st_v8(void *p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// N consecutive values; VEC: the address is 32-byte aligned and N * sizeof(T) a multiple of 32.
 template <class T, int N, bool VEC>
 __device__ __forceinline__ void load_row(const T *p, float (&v)[N]) {
-    if (VEC) {
-        constexpr int PER = 16 / sizeof(T);
+    if constexpr (VEC) {
+        constexpr int PER = 32 / sizeof(T);
 #pragma unroll
         for (int i = 0; i < N / PER; ++i) {
-            const uint4 u = ld_stream_v4(p + i * PER);
-            const T *t = reinterpret_cast<const T *>(&u);
+            uint32_t u[8];
+            ld_stream_v8(p + i * PER, u);
+            const T *t = reinterpret_cast<const T *>(u);
 #pragma unroll
             for (int j = 0; j < PER; ++j) v[i * PER + j] = to_f32<T>(t[j]);
         }
@@ -69,15 +82,15 @@ __device__ __forceinline__ void load_row(const T *p, float (&v)[N]) {
 }
 template <class T, int N, bool VEC>
 __device__ __forceinline__ void store_row(T *p, const float (&v)[N]) {
-    if (VEC) {
-        constexpr int PER = 16 / sizeof(T);
+    if constexpr (VEC) {
+        constexpr int PER = 32 / sizeof(T);
 #pragma unroll
         for (int i = 0; i < N / PER; ++i) {
-            uint4 u;
-            T *t = reinterpret_cast<T *>(&u);
+            uint32_t u[8];
+            T *t = reinterpret_cast<T *>(u);
 #pragma unroll
             for (int j = 0; j < PER; ++j) t[j] = from_f32<T>(v[i * PER + j]);
-            reinterpret_cast<uint4 *>(p)[i] = u;
+            st_v8(p + i * PER, u);
         }
     } else {
 #pragma unroll
@@ -85,67 +98,84 @@ __device__ __forceinline__ void store_row(T *p, const float (&v)[N]) {
     }
 }
 
+// Rows cut into segments of items, a CTA per segment (rows * segments CTAs): item i of a row on
+// thread i % blockDim.x.  Keeps a row's index arithmetic out of the items.
+struct RowSplit {
+    int items, segments, per;   // items a row, segments a row, items a segment
+    __device__ __forceinline__ void place(int &row, int &first, int &last) const {
+        row = segments == 1 ? blockIdx.x : blockIdx.x / segments;
+        const int s = blockIdx.x - row * segments;
+        first = s * per;
+        last = min(items, first + per);
+    }
+};
+
 // ------------------------------------------------------------------ quantise
-// A thread takes 8 inputs, four threads a block of 32.  Row r goes to row r of the output, or
-// to the rows inv_pos[r * k + j], j < k (entries outside [0, out_rows) are skipped).
+// A thread takes 16 inputs (one or two 32-byte loads), two neighbours a block of 32.  Row r goes
+// to row r of the output, or to the rows inv_pos[r * k + j], j < k (entries outside [0, out_rows)
+// are skipped): the row is read and rounded once however many places it goes to.  Bound by
+// memory: bytes read once, written k times.
 template <class T, bool VEC>
-__global__ void __launch_bounds__(256) mxfp4_quantize_kernel(const T *__restrict__ x, int64_t ld, int rows, int K,
+__global__ void __launch_bounds__(128) mxfp4_quantize_kernel(const T *__restrict__ x, int64_t ld, int K, RowSplit split,
                                                              const int *__restrict__ inv_pos, int k, int out_rows,
                                                              uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
-    const int per_row = K / 8;
-    const int64_t total = (int64_t)rows * per_row;
-    // total is a multiple of four: the threads of a block of 32 inputs are all in or all out
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int r = (int)(i / per_row), g = (int)(i - (int64_t)r * per_row);
-        float v[8];
-        load_row<T, 8, VEC>(x + r * ld + g * 8, v);
+    int r, first, last;
+    split.place(r, first, last);
+    // items are K / 16 and segments even: the two threads of a block of 32 are in or out together
+    for (int g = first + threadIdx.x; g < last; g += blockDim.x) {
+        float v[16];
+        load_row<T, 16, VEC>(x + r * ld + g * 16, v);
         uint32_t amax = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
-        const unsigned team = 0xfu << (threadIdx.x & 28);
-        amax = max(amax, __shfl_xor_sync(team, amax, 1));
-        amax = max(amax, __shfl_xor_sync(team, amax, 2));
+        for (int j = 0; j < 16; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+        amax = max(amax, __shfl_xor_sync(3u << (threadIdx.x & 30), amax, 1));
         const uint32_t s = mx_scale_byte(amax);
-        uint32_t c = 0x77777777u;
+        uint2 c = make_uint2(0x77777777u, 0x77777777u);
         if (s != 255u) {
             const float inv = mx_inverse(s);
-            c = 0;
+            c = make_uint2(0, 0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c |= e2m1x2_code(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
+            for (int j = 0; j < 4; ++j) {
+                c.x |= e2m1x2_code(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
+                c.y |= e2m1x2_code(v[8 + 2 * j] * inv, v[9 + 2 * j] * inv) << (8 * j);
+            }
         }
+        const size_t code_at = (size_t)g * 8, scale_at = g >> 1;
         if (!inv_pos) {
-            *reinterpret_cast<uint32_t *>(codes + (size_t)r * (K / 2) + g * 4) = c;
-            if ((g & 3) == 0) scales[(size_t)r * (K / MX_BLOCK) + (g >> 2)] = (uint8_t)s;
+            *reinterpret_cast<uint2 *>(codes + (size_t)r * (K / 2) + code_at) = c;
+            if ((g & 1) == 0) scales[(size_t)r * (K / MX_BLOCK) + scale_at] = (uint8_t)s;
         } else {
+#pragma unroll 4
             for (int j = 0; j < k; ++j) {
-                const int p = inv_pos[(size_t)r * k + j];
+                const int p = __ldg(inv_pos + (size_t)r * k + j);
                 if (p < 0 || p >= out_rows) continue;
-                *reinterpret_cast<uint32_t *>(codes + (size_t)p * (K / 2) + g * 4) = c;
-                if ((g & 3) == 0) scales[(size_t)p * (K / MX_BLOCK) + (g >> 2)] = (uint8_t)s;
+                *reinterpret_cast<uint2 *>(codes + (size_t)p * (K / 2) + code_at) = c;
+                if ((g & 1) == 0) scales[(size_t)p * (K / MX_BLOCK) + scale_at] = (uint8_t)s;
             }
         }
     }
 }
 
 // ------------------------------------------------------------------ dequantise
+// A thread takes 16 values: 8 bytes of codes and their scale byte to one or two 32-byte stores.
 template <class T, bool VEC>
-__global__ void __launch_bounds__(256) mxfp4_dequantize_kernel(const uint8_t *__restrict__ codes,
-                                                               const uint8_t *__restrict__ scales, int rows, int K,
+__global__ void __launch_bounds__(128) mxfp4_dequantize_kernel(const uint8_t *__restrict__ codes,
+                                                               const uint8_t *__restrict__ scales, int K, RowSplit split,
                                                                T *__restrict__ out, int64_t ld) {
-    const int per_row = K / 8;
-    const int64_t total = (int64_t)rows * per_row;
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int r = (int)(i / per_row), g = (int)(i - (int64_t)r * per_row);
-        const uint32_t c = __ldg(reinterpret_cast<const uint32_t *>(codes + (size_t)r * (K / 2)) + g);
-        const float s = e8m0_value(scales[(size_t)r * (K / MX_BLOCK) + (g >> 2)]);
-        float v[8];
+    int r, first, last;
+    split.place(r, first, last);
+#pragma unroll 2
+    for (int g = first + threadIdx.x; g < last; g += blockDim.x) {
+        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes + (size_t)r * (K / 2)) + g);
+        const float s = e8m0_value(__ldg(scales + (size_t)r * (K / MX_BLOCK) + (g >> 1)));
+        float v[16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(e2m1x2_value((c >> (8 * j)) & 0xFFu));
+        for (int j = 0; j < 8; ++j) {
+            const float2 f = __half22float2(e2m1x2_value(((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 0xFFu));
             v[2 * j] = f.x * s;
             v[2 * j + 1] = f.y * s;
         }
-        store_row<T, 8, VEC>(out + r * ld + g * 8, v);
+        store_row<T, 16, VEC>(out + r * ld + g * 16, v);
     }
 }
 

@@ -76,6 +76,17 @@ struct OnDevice {
     }
 };
 
+bool aligned32(const void *p) { return ((uintptr_t)p & 31u) == 0; }
+
+// CTAs of 128 threads: an item a thread where there are few, up to `most` where there are many
+// (a row's index arithmetic and indexes are then shared by its items).
+RowSplit split_rows(int64_t rows, int items, int most) {
+    int each = (int)std::min<int64_t>(std::max<int64_t>(rows * items / (148 * 2048), 1), most);
+    RowSplit s{items, (items + 128 * each - 1) / (128 * each), 0};
+    if (rows * s.segments > INT32_MAX) s.segments = 1;
+    s.per = ((items + s.segments - 1) / s.segments + 1) & ~1;
+    return s;
+}
 int blocks_for(int64_t threads) { return (int)std::min<int64_t>((threads + 255) / 256, 148 * 64); }
 
 // ------------------------------------------------------------------ routing from logits
@@ -228,10 +239,10 @@ ds4moe_status ds4moe_mxfp4_quantize(const void *x_dev, int32_t x_type, int64_t l
     if (rows == 0 || out_rows == 0) return DS4MOE_OK;
     if (!x_dev || (uintptr_t)x_dev % size_of(x_type) || !codes_dev || !aligned16(codes_dev) || !scales_dev) return DS4MOE_EINVAL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
-    const bool vec = aligned16(x_dev) && ld * size_of(x_type) % 16 == 0;
-    const int grid = blocks_for((int64_t)rows * (K / 8));
+    const bool vec = aligned32(x_dev) && ld * size_of(x_type) % 32 == 0;
+    const RowSplit split = split_rows(rows, K / 16, 4);
     auto go = [&](auto kernel, auto *x) {
-        kernel<<<grid, 256, 0, st>>>(x, ld, rows, K, inv_pos_dev, top_k, out_rows, codes_dev, scales_dev);
+        kernel<<<rows * split.segments, 128, 0, st>>>(x, ld, K, split, inv_pos_dev, top_k, out_rows, codes_dev, scales_dev);
     };
     if (x_type == DS4MOE_F32) {
         auto *x = static_cast<const float *>(x_dev);
@@ -253,9 +264,11 @@ ds4moe_status ds4moe_mxfp4_dequantize(const uint8_t *codes_dev, const uint8_t *s
     if (rows == 0) return DS4MOE_OK;
     if (!codes_dev || !aligned16(codes_dev) || !scales_dev || !out_dev || (uintptr_t)out_dev % size_of(out_type)) return DS4MOE_EINVAL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
-    const bool vec = aligned16(out_dev) && ld * size_of(out_type) % 16 == 0;
-    const int grid = blocks_for((int64_t)rows * (K / 8));
-    auto go = [&](auto kernel, auto *out) { kernel<<<grid, 256, 0, st>>>(codes_dev, scales_dev, rows, K, out, ld); };
+    const bool vec = aligned32(out_dev) && ld * size_of(out_type) % 32 == 0;
+    const RowSplit split = split_rows(rows, K / 16, 4);
+    auto go = [&](auto kernel, auto *out) {
+        kernel<<<rows * split.segments, 128, 0, st>>>(codes_dev, scales_dev, K, split, out, ld);
+    };
     if (out_type == DS4MOE_F32) {
         auto *o = static_cast<float *>(out_dev);
         if (vec) go(mxfp4_dequantize_kernel<float, true>, o); else go(mxfp4_dequantize_kernel<float, false>, o);
@@ -283,13 +296,18 @@ ds4moe_status ds4moe_combine(const void *o_dev, int32_t o_type, int64_t o_rows, 
         return DS4MOE_EINVAL;
     CombineArgs a{o_dev, o_rows, T, top_k, H, inv_pos_dev, topk_w_dev, add_dev, add_type, y_dev};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
-    const int grid = blocks_for((int64_t)T * H);
-    auto go = [&](auto kernel) { kernel<<<grid, 256, 0, st>>>(a); };
+    const int64_t per = 32 / size_of(o_type);   // columns of a 32-byte piece
+    const bool vec = H % per == 0 && aligned32(o_dev) && H * size_of(o_type) % 32 == 0 && aligned32(y_dev) &&
+                     H * size_of(y_type) % 16 == 0 && (!add_dev || aligned16(add_dev));
+    const RowSplit split = split_rows(T, vec ? H / per : H, 4);
+    auto go = [&](auto wide, auto columns) {
+        (vec ? wide : columns)<<<T * split.segments, 128, 0, st>>>(a, split);
+    };
     auto with = [&](auto o) {
         using TO = decltype(o);
-        if (y_type == DS4MOE_F32) go(combine_kernel<TO, float>);
-        else if (y_type == DS4MOE_BF16) go(combine_kernel<TO, __nv_bfloat16>);
-        else go(combine_kernel<TO, __half>);
+        if (y_type == DS4MOE_F32) go(combine_kernel<TO, float>, combine_columns_kernel<TO, float>);
+        else if (y_type == DS4MOE_BF16) go(combine_kernel<TO, __nv_bfloat16>, combine_columns_kernel<TO, __nv_bfloat16>);
+        else go(combine_kernel<TO, __half>, combine_columns_kernel<TO, __half>);
     };
     if (o_type == DS4MOE_F32) with(float{});
     else if (o_type == DS4MOE_BF16) with(__nv_bfloat16{});
