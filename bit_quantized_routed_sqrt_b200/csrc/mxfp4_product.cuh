@@ -55,8 +55,9 @@ constexpr int MX_CHUNK = 32;             // rows of a (accumulator columns) that
 constexpr int MX_PAIR_BYTES = 2 * (32 * 16 + 2 * 32);
 
 // BOX1 < BOX0 < NT: the row counts that one TMA load can bring (a tile takes the least that holds it).
-template <int NT_, int BOX0_, int BOX1_, int STAGES_, bool GATED_>
+template <int NT_, int BOX0_, int BOX1_, int STAGES_, int CTAS_, bool GATED_>
 struct MxCfg {
+    static constexpr int CTAS = CTAS_;   // a SM
     static constexpr int NT = NT_, BOX0 = BOX0_, BOX1 = BOX1_, STAGES = STAGES_;
     static constexpr bool GATED = GATED_;
     static constexpr int SF_CHUNKS = (NT + 127) / 128;                 // 512-byte scale chunks of the rows per 128 inputs
@@ -75,7 +76,7 @@ struct MxCfg {
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES + S_BYTES;
     static_assert(COLS <= 512, "tensor memory");
     static_assert(STAGES >= 4, "a scale warp waits on every other pair of steps, at most 3 steps apart");
-    static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+    static_assert(CTAS * (SMEM + 1024) <= 228 * 1024 && CTAS * TMEM <= 512, "shared and tensor memory of a SM");
     static_assert(NT % 16 == 0 && NT > BOX0 && BOX0 > BOX1 && BOX1 % 8 == 0, "row tiles");
     static_assert((2 * STAGES + 5) * 8 + 16 + 32 + 4 * STAGES <= BAR_BYTES, "barrier area");
 };
@@ -260,7 +261,7 @@ __device__ __forceinline__ void mx_store_chunk_mxfp4(const MxArgs &p, const floa
 }
 
 template <class C>
-__global__ void __launch_bounds__(MX_THREADS, 1)
+__global__ void __launch_bounds__(MX_THREADS, C::CTAS)
     mxfp4_product_kernel(const __grid_constant__ CUtensorMap tm_nt, const __grid_constant__ CUtensorMap tm_box0,
                          const __grid_constant__ CUtensorMap tm_box1, const __grid_constant__ MxArgs p) {
     extern __shared__ __align__(1024) uint8_t mx_smem_raw[];

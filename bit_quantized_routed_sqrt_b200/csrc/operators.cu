@@ -136,22 +136,22 @@ bool row_map(CUtensorMap *m, const void *codes, int rows, int K, int box_rows) {
 template <class C>
 ds4moe_status run_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
     const int64_t row_tiles = a.rows / C::NT + a.E, m_tiles = ((int64_t)a.N * (a.gated ? 2 : 1) + MX_TM - 1) / MX_TM;
-    if (row_tiles * m_tiles + h->num_sms > INT32_MAX) return fail(h, DS4MOE_EINVAL, "too many tiles for one call");
+    if (row_tiles * m_tiles + h->num_sms * C::CTAS > INT32_MAX) return fail(h, DS4MOE_EINVAL, "too many tiles for one call");
     CUtensorMap tm[3];
     const int boxes[3] = {C::NT, C::BOX0, C::BOX1};
     for (int i = 0; i < 3; ++i)
         if (!row_map(&tm[i], a.a_codes, a.rows, a.K, boxes[i])) return fail(h, DS4MOE_ECUDA, "tensor map of the rows");
     CK(h, cudaFuncSetAttribute(mxfp4_product_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM));
-    mxfp4_product_kernel<C><<<h->num_sms, MX_THREADS, C::SMEM, st>>>(tm[0], tm[1], tm[2], a);
+    mxfp4_product_kernel<C><<<h->num_sms * C::CTAS, MX_THREADS, C::SMEM, st>>>(tm[0], tm[1], tm[2], a);
     CK(h, cudaGetLastError());
     return DS4MOE_OK;
 }
 template <bool GATED>
 ds4moe_status pick_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
     const double per_expert = (double)a.rows / std::min(a.rows, a.E);
-    if (per_expert <= 24) return run_product<MxCfg<32, 16, 8, 8, GATED>>(h, a, st);
-    if (per_expert <= 112) return run_product<MxCfg<128, 64, 32, 5, GATED>>(h, a, st);
-    return run_product<MxCfg<192, 128, 64, 5, GATED>>(h, a, st);
+    if (per_expert <= 24) return run_product<MxCfg<32, 16, 8, 8, 1, GATED>>(h, a, st);
+    if (per_expert <= 112) return run_product<MxCfg<128, 64, 32, 5, 1, GATED>>(h, a, st);
+    return run_product<MxCfg<192, 128, 64, 5, 1, GATED>>(h, a, st);
 }
 
 }  // namespace
@@ -299,15 +299,19 @@ ds4moe_status ds4moe_combine(const void *o_dev, int32_t o_type, int64_t o_rows, 
     const int64_t per = 32 / size_of(o_type);   // columns of a 32-byte piece
     const bool vec = H % per == 0 && aligned32(o_dev) && H * size_of(o_type) % 32 == 0 && aligned32(y_dev) &&
                      H * size_of(y_type) % 16 == 0 && (!add_dev || aligned16(add_dev));
-    const RowSplit split = split_rows(T, vec ? H / per : H, 4);
-    auto go = [&](auto wide, auto columns) {
-        (vec ? wide : columns)<<<T * split.segments, 128, 0, st>>>(a, split);
-    };
+    const int piece = 16 / size_of(o_type);
+    const RowSplit split = split_rows(T, vec ? H / per : (H + piece - 1) / piece, 4);
+    auto go = [&](auto kernel) { kernel<<<T * split.segments, 128, 0, st>>>(a, split); };
     auto with = [&](auto o) {
         using TO = decltype(o);
-        if (y_type == DS4MOE_F32) go(combine_kernel<TO, float>, combine_columns_kernel<TO, float>);
-        else if (y_type == DS4MOE_BF16) go(combine_kernel<TO, __nv_bfloat16>, combine_columns_kernel<TO, __nv_bfloat16>);
-        else go(combine_kernel<TO, __half>, combine_columns_kernel<TO, __half>);
+        auto to = [&](auto y) {
+            using TY = decltype(y);
+            if (vec) go(combine_kernel<TO, TY>);
+            else go(combine_shifted_kernel<TO, TY>);
+        };
+        if (y_type == DS4MOE_F32) to(float{});
+        else if (y_type == DS4MOE_BF16) to(__nv_bfloat16{});
+        else to(__half{});
     };
     if (o_type == DS4MOE_F32) with(float{});
     else if (o_type == DS4MOE_BF16) with(__nv_bfloat16{});
