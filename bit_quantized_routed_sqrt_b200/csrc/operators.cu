@@ -104,11 +104,11 @@ int route_block(int T) {
     while (TB < SR_MAX_BLOCK && T / TB > 592) TB *= 2;
     return TB;
 }
-// Counts and masks of every block, and the totals.
+// Counts of every block, the totals, and the blocks' masks.
 size_t route_workspace(const ds4moe_router *r, int T) {
     const int TB = route_block(T);
-    const size_t NB = ((size_t)T + TB - 1) / TB;
-    return NB <= 1 ? 0 : (NB * (1 + TB / 32) + 1) * r->n_experts * 4;
+    const size_t NB = ((size_t)T + TB - 1) / TB, pitch = (r->n_experts + 3) / 4 * 4;
+    return NB <= 1 ? 0 : ((NB + 1) * pitch + NB * (TB / 32) * r->n_experts) * 4;
 }
 
 // ------------------------------------------------------------------ MXFP4 products
@@ -188,15 +188,17 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
     a.topk_idx = topk_idx_dev; a.topk_w = topk_w_dev;
     a.offsets = expert_offsets_dev; a.sorted_token = sorted_token_dev; a.sorted_slot = sorted_slot_dev; a.inv_pos = inv_pos_dev;
     if (permute && a.NB > 1) {
-        if (!workspace_dev || (uintptr_t)workspace_dev % 4 || workspace_bytes < route_workspace(r, T)) return DS4MOE_EINVAL;
+        if (!workspace_dev || !aligned16(workspace_dev) || workspace_bytes < route_workspace(r, T)) return DS4MOE_EINVAL;
         a.cnt = static_cast<int *>(workspace_dev);
-        a.total = a.cnt + (size_t)a.NB * a.E;
-        a.mask = reinterpret_cast<uint32_t *>(a.total + a.E);
+        a.pitch = (a.E + 3) / 4 * 4;
+        a.total = a.cnt + (size_t)a.NB * a.pitch;
+        a.mask = reinterpret_cast<uint32_t *>(a.total + a.pitch);
     }
-    // one block: enough warps for its tokens
-    const int warps = a.NB > 1 ? SR_WARPS : std::min(std::max(T, SR_WARPS), SR_MAX_WARPS);
+    // one block, or fewer than the SMs: more warps a block, two tokens a warp
+    const bool few = a.NB <= 148;
+    const int warps = few ? std::min(std::max(std::min(T, a.TB) / 2, SR_WARPS), SR_MAX_WARPS) : SR_WARPS;
     auto launch = [&](auto many, auto lone, int npl) {
-        auto kernel = a.NB > 1 ? many : lone;
+        auto kernel = few ? lone : many;
         const size_t smem = (a.G > 1 ? (size_t)warps * 32 * npl * 8 : 0) + (size_t)a.E * (a.TB / 32 + 1) * 4;
         if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         kernel<<<a.NB, 32 * warps, smem, st>>>(a);
@@ -226,7 +228,10 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
         scored_scan_kernel<<<(a.E + 31) / 32, 1024, 0, st>>>(a);
         if ((s = launched()) != DS4MOE_OK) return s;
     }
-    scored_permute_kernel<<<a.NB, SCAN_THREADS, (size_t)a.E * (a.TB / 32 + 2) * 4, st>>>(a, scanned);
+    const size_t sums = scanned ? 0 : (size_t)2 * (SR_PERMUTE_THREADS / (a.pitch / 4)) * a.pitch;
+    static_assert((2 * SR_MAX_EXPERTS + 2 * 4 * SR_PERMUTE_THREADS + SR_MAX_EXPERTS * (SR_MAX_BLOCK / 32)) * 4 <= 48 * 1024,
+                  "shared memory of the permutation");
+    scored_permute_kernel<<<a.NB, SR_PERMUTE_THREADS, (2 * a.pitch + sums + (size_t)a.E * (a.TB / 32)) * 4, st>>>(a, scanned);
     return launched();
 }
 

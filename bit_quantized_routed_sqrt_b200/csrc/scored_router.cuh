@@ -10,7 +10,8 @@ constexpr int SR_MAX_TOPK = 32;
 constexpr int SR_MAX_GROUPS = 32;
 constexpr int SR_MIN_BLOCK = 32, SR_MAX_BLOCK = 256;     // tokens a CTA
 constexpr int SR_WARPS = 8, SR_MAX_WARPS = 16;           // warps a CTA (a lone CTA: up to 16)
-constexpr int SR_DIRECT = 128;                           // blocks whose counts every CTA adds up itself
+constexpr int SR_DIRECT = 256;                           // blocks whose counts every CTA adds up itself
+constexpr int SR_PERMUTE_THREADS = 512;
 
 enum : int { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1, SCORE_SQRT_SOFTPLUS = 2 };
 
@@ -25,8 +26,9 @@ struct ScoredArgs {
     int *topk_idx;           // [T][k]
     float *topk_w;
     int *offsets, *sorted_token, *sorted_slot, *inv_pos;   // each may be null
-    int *cnt;                // workspace [NB][E]
-    uint32_t *mask;          // workspace [NB][E][TB / 32]
+    int pitch;               // E rounded up to 4
+    int *cnt;                // workspace [NB][pitch], 16-byte aligned
+    uint32_t *mask;          // workspace [NB][E][words of TB bits]
     int *total;              // workspace [E]
 };
 
@@ -53,19 +55,18 @@ __device__ __forceinline__ void warp_best(double &v, int &i) {
     }
 }
 
-// The choice of one token in fp64, by one warp; lane holds experts lane + 32 i.  Returns to
-// lane j < k the expert of slot j (-1: no candidate was left).  About 3000 instructions a
-// token at 256 experts: it runs where scored_choice and scored_rank cannot tell.
+// One token's exact values in fp64, by one warp; lane holds experts lane + 32 i.  Returns the mask
+// of the groups that the token may choose from, and to each lane its experts' choice values
+// (-inf: no candidate, or not in those groups).
 template <int NPL>
-__device__ __noinline__ int scored_choice64(const ScoredArgs &p, int64_t t, double *scratch) {
+__device__ __forceinline__ unsigned scored_values64(const ScoredArgs &p, int64_t t, double *scratch, double (&c)[NPL]) {
     const int lane = threadIdx.x & 31;
-    double l[NPL], c[NPL];
+    double l[NPL];
     double m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         const int e = lane + 32 * i;
         const float v = e < p.E ? load_typed(p.logits, p.type, t * p.ld + e) : -INFINITY;
-        // NaN and -inf: no candidate.  +inf counts as the largest finite value.
         l[i] = v > -INFINITY ? (double)fminf(v, 3.402823466e38f) : -INFINITY;
         m = fmax(m, l[i]);
     }
@@ -89,37 +90,50 @@ __device__ __noinline__ int scored_choice64(const ScoredArgs &p, int64_t t, doub
             if (!(c[i] > -INFINITY)) c[i] = l[i] = -INFINITY;
         }
     }
-    if (p.G > 1) {
-        const int per = p.E / p.G;
-        __syncwarp();
+    if (p.G == 1) return 1u;
+    const int per = p.E / p.G;
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (lane + 32 * i < p.E) scratch[lane + 32 * i] = c[i];
-        __syncwarp();
-        double best = -INFINITY, next = -INFINITY;
-        if (lane < p.G)
-            for (int j = 0; j < per; ++j) {
-                const double v = scratch[lane * per + j];
-                if (v > best) { next = best; best = v; }
-                else if (v > next) next = v;
-            }
-        double g = p.top2 && next > -INFINITY ? best + next : best;
-        unsigned kept = 0;
-        for (int j = 0; j < p.topk_groups; ++j) {
-            double v = g;
-            int gi = lane;
-            warp_best(v, gi);
-            if (!(v > -INFINITY)) break;
-            kept |= 1u << gi;
-            if (lane == gi) g = -INFINITY;
+    for (int i = 0; i < NPL; ++i)
+        if (lane + 32 * i < p.E) scratch[lane + 32 * i] = c[i];
+    __syncwarp();
+    double best = -INFINITY, next = -INFINITY;
+    if (lane < p.G)
+        for (int j = 0; j < per; ++j) {
+            const double v = scratch[lane * per + j];
+            next = fmax(next, fmin(best, v));
+            best = fmax(best, v);
         }
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int e = lane + 32 * i;
-            if (e < p.E && !((kept >> (e / per)) & 1u)) c[i] = -INFINITY;
-            else if (!p.bias) c[i] = l[i];
-        }
+    const double g = p.top2 && next > -INFINITY ? best + next : best;
+    int rank = 0;
+    for (int h = 0; h < p.G; ++h) {
+        const double o = __shfl_sync(0xffffffffu, g, h);
+        rank += o > g || (o == g && h < lane);
     }
+    const unsigned kept = __ballot_sync(0xffffffffu, g > -INFINITY && rank < p.topk_groups);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = lane + 32 * i;
+        if (e < p.E && !((kept >> (e / per)) & 1u)) c[i] = -INFINITY;
+        else if (!p.bias) c[i] = l[i];
+    }
+    return kept;
+}
+
+// The groups of one token, exactly: for scored_choice, where two groups are too close.
+template <int NPL>
+__device__ __noinline__ unsigned scored_groups64(const ScoredArgs &p, int64_t t, double *scratch) {
+    double c[NPL];
+    return scored_values64<NPL>(p, t, scratch, c);
+}
+
+// The choice of one token in fp64: to lane j < k the expert of slot j (-1: no candidate was
+// left).  It runs where scored_choice and scored_rank cannot tell.
+template <int NPL>
+__device__ __noinline__ int scored_choice64(const ScoredArgs &p, int64_t t, double *scratch) {
+    const int lane = threadIdx.x & 31;
+    double c[NPL];
+    scored_values64<NPL>(p, t, scratch, c);
     int my_e = -1;
     for (int j = 0; j < p.k; ++j) {
         double v = -INFINITY;
@@ -145,8 +159,8 @@ __device__ __noinline__ int scored_choice64(const ScoredArgs &p, int64_t t, doub
 // a slot is then one warp maximum over the lanes' heads and a shift in the lane that had it.
 // The order is certain where neighbours (the first expert left out among them) differ by more
 // than 2 M and the cut; where some are closer, exact ties of fp32 logits among them, scored_rank
-// orders all that may be among the first k by their fp64 values, and scored_choice64 does the
-// whole token where groups are too close or the candidates too many.  Without a bias the values are the logits themselves: M is 0, and for fp16
+// orders all that may be among the first k by their fp64 values (scored_choice64 does the whole
+// token where they are too many); where groups are too close, scored_groups64 chooses them.  Without a bias the values are the logits themselves: M is 0, and for fp16
 // and bf16 logits the cut drops nothing, so nothing is left to decide.
 
 constexpr uint32_t SR_LIVE = 0x00800000u;   // the lowest key of a finite value
@@ -246,7 +260,7 @@ struct LaneLogits {
         } else {
             x = (threadIdx.x & 31) + 32 * i < p.E ? to_f32<T>(v[i]) : -INFINITY;
         }
-        return x > -INFINITY ? fminf(x, 3.402823466e38f) : -INFINITY;
+        return fminf(fmaxf(x, -INFINITY), 3.402823466e38f);   // fmaxf drops a NaN
     }
 };
 
@@ -286,10 +300,10 @@ __device__ __noinline__ int scored_rank(const ScoredArgs &p, int64_t t, const La
 }
 
 // The choice of one token by one warp: to lane j < k the expert of slot j, or -1.  bias: the
-// lane's experts' (if any).
+// lane's experts' (0 without one, -inf for a NaN); bias_size: the largest magnitude of all.
 template <int NPL, class T, bool VEC>
 __device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, const LaneLogits<NPL, T, VEC> &logits,
-                                             const float (&bias)[NPL], double *scratch) {
+                                             const float (&bias)[NPL], float bias_size, double *scratch) {
     using L = LaneLogits<NPL, T, VEC>;
     constexpr uint32_t LOW = NPL <= 8 ? 255u : 511u;   // room for the index
     const int lane = threadIdx.x & 31;
@@ -303,40 +317,41 @@ __device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, con
         // each, the series' roundings 2^-22; a root halves what comes before it), 4 more where a
         // sum of 512 is in it (13 additions, its terms' errors, its reciprocal), and the sum with
         // the bias is off by 2^-24; below e^-87 the exponentials may be flushed to 0, a score (a
-        // root) of up to 1.3e-19.
-        float off = 0.0f, size = 0.0f;
-        auto take = [&](int i, float s, float weight) {   // a score and (4 or 8 + |x|)
-            const bool live = a[i] > -INFINITY;
-            off = fmaxf(off, live ? s * weight : 0.0f);
-            if (p.bias) s += bias[i];
-            a[i] = live && s > -INFINITY ? s : -INFINITY;
-            size = fmaxf(size, live ? fabsf(s) : 0.0f);   // of a NaN: not taken
-        };
+        // root) of up to 1.3e-19.  Score times (4 or 8 + |x|) grows with the logit, whichever the
+        // score, so the largest logit's bounds every expert's.
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) top = fmaxf(top, a[i]);
+        top = fmaxf(warp_max_f32(top), -3.402823466e38f);
+        float most, off;   // the largest score, and it times (4 or 8 + |x|)
+        auto take = [&](int i, float s) { a[i] = a[i] > -INFINITY ? s + bias[i] : -INFINITY; };
         // (one loop for each score: a test inside the loop costs as much as a score)
         if (p.score == SCORE_SOFTMAX) {
-            float top = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) top = fmaxf(top, a[i]);
-            top = fmaxf(warp_max_f32(top), -3.402823466e38f);
             float sum = 0.0f, e[NPL];
 #pragma unroll
             for (int i = 0; i < NPL; ++i) sum += e[i] = approx_exp(a[i] - top);   // of -inf: 0
-            const float scale = approx_rcp(warp_sum(sum));
+            most = approx_rcp(warp_sum(sum));
+            off = 8.0f * most;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) take(i, e[i] * scale, 8.0f - (a[i] - top));
+            for (int i = 0; i < NPL; ++i) take(i, e[i] * most);
         } else if (p.score == SCORE_SIGMOID) {
+            auto score = [](float l) { return approx_rcp(1.0f + approx_exp(-l)); };
+            most = score(top);
+            off = most * (4.0f + fabsf(top));
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) take(i, approx_rcp(1.0f + approx_exp(-a[i])), 4.0f + fabsf(a[i]));
+            for (int i = 0; i < NPL; ++i) take(i, score(a[i]));
         } else {
+            auto score = [](float l) {
+                const float ex = approx_exp(-fabsf(l));
+                return approx_sqrt(fmaxf(l, 0.0f) + log1p_unit(ex, approx_rcp(2.0f + ex)));
+            };
+            most = score(top);
+            off = most * (4.0f + fabsf(top));
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                const float ex = approx_exp(-fabsf(a[i]));
-                take(i, approx_sqrt(fmaxf(a[i], 0.0f) + log1p_unit(ex, approx_rcp(2.0f + ex))), 4.0f + fabsf(a[i]));
-            }
+            for (int i = 0; i < NPL; ++i) take(i, score(a[i]));
         }
-        M = warp_max_f32(fmaf(off, 2.384185791e-7f, fmaf(size, 1.192092896e-7f, 2e-19f)));
+        M = fmaf(off, 2.384185791e-7f, fmaf(most + bias_size, 1.192092896e-7f, 2e-19f));
     }
-    bool sure = true;
     uint32_t key[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
@@ -366,11 +381,12 @@ __device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, con
             rank += o > g || (o == g && h < lane);
         }
         const bool in = g > -INFINITY && rank < p.topk_groups;
-        const unsigned kept = __ballot_sync(0xffffffffu, in);
+        unsigned kept = __ballot_sync(0xffffffffu, in);
         if (by_score) {
             const float least = -warp_max_f32(in ? -g : -INFINITY);
             const float left = warp_max_f32(!in ? g : -INFINITY);
-            sure = !(left > -INFINITY) || least - left > 4.0f * M + 2.4e-7f * (fabsf(least) + fabsf(left));
+            if (left > -INFINITY && !(least - left > 4.0f * M + 2.4e-7f * (fabsf(least) + fabsf(left))))
+                kept = scored_groups64<NPL>(p, t, scratch);
         }
         const float inv = 1.0f / (float)per;
 #pragma unroll
@@ -383,15 +399,13 @@ __device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, con
         }
         if (!p.bias) M = 0.0f;
     }
-    if (!sure) return scored_choice64<NPL>(p, t, scratch);
     sort_network<NPL>(key);
     auto pop = [&]() {   // the best key left, taken out
         const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
-        if (key[0] == best) {
+        const bool had = key[0] == best;
 #pragma unroll
-            for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1];
-            key[NPL - 1] = 0u;
-        }
+        for (int i = 0; i + 1 < NPL; ++i) key[i] = had ? key[i + 1] : key[i];
+        key[NPL - 1] = had ? 0u : key[NPL - 1];
         return best;
     };
     uint32_t mine = 0, last = 0;
@@ -511,18 +525,20 @@ __global__ void __launch_bounds__(32 * (LONE ? SR_MAX_WARPS : SR_WARPS), LONE ||
     const int t0 = blockIdx.x * p.TB, nt = min(p.TB, p.T - t0);
     LaneLogits<NPL, T, VEC> now, next;
     if (warp < nt) next.load(p, t0 + warp);
-    float bias[NPL];
+    float bias[NPL], bias_size = 0.0f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         const int e = LaneLogits<NPL, T, VEC>::expert(lane, i);
-        bias[i] = p.bias && e < p.E ? p.bias[e] : 0.0f;
+        bias[i] = p.bias && e < p.E ? fmaxf(p.bias[e], -INFINITY) : 0.0f;   // fmaxf drops a NaN
+        if (bias[i] > -INFINITY) bias_size = fmaxf(bias_size, fabsf(bias[i]));
     }
+    bias_size = warp_max_f32(bias_size);
     for (int i = threadIdx.x; i < p.E * W; i += blockDim.x) mask[i] = 0;
     __syncthreads();
     for (int tl = warp; tl < nt; tl += warps) {
         now = next;
         if (tl + warps < nt) next.load(p, t0 + tl + warps);
-        const int e = scored_choice<NPL, T, VEC>(p, t0 + tl, now, bias, scratch + (p.G > 1 ? warp * 32 * NPL : 0));
+        const int e = scored_choice<NPL, T, VEC>(p, t0 + tl, now, bias, bias_size, scratch + (p.G > 1 ? warp * 32 * NPL : 0));
         const float w = scored_weight<NPL, T, VEC>(p, t0 + tl, now, e);
         if (lane < p.k) {
             const size_t pair = (size_t)(t0 + tl) * p.k + lane;
@@ -537,7 +553,7 @@ __global__ void __launch_bounds__(32 * (LONE ? SR_MAX_WARPS : SR_WARPS), LONE ||
         int n = 0;
         for (int w = 0; w < W; ++w) n += __popc(mask[e * W + w]);
         base[e] = n;
-        if (p.NB > 1) p.cnt[(size_t)blockIdx.x * p.E + e] = n;
+        if (p.NB > 1) p.cnt[(size_t)blockIdx.x * p.pitch + e] = n;
     }
     if (p.NB > 1) {
         for (int i = threadIdx.x; i < p.E * W; i += blockDim.x) p.mask[(size_t)blockIdx.x * p.E * W + i] = mask[i];
@@ -563,7 +579,7 @@ __global__ void __launch_bounds__(1024) scored_scan_kernel(const __grid_constant
         const int each = (min(p.NB - b0, 512) + 31) / 32, first = b0 + warp * each;
         int v[16], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = on && i < each && first + i < p.NB ? p.cnt[(size_t)(first + i) * p.E + e] : 0;
+        for (int i = 0; i < 16; ++i) v[i] = on && i < each && first + i < p.NB ? p.cnt[(size_t)(first + i) * p.pitch + e] : 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum += v[i];
         sums[warp][lane] = sum;
@@ -577,7 +593,7 @@ __global__ void __launch_bounds__(1024) scored_scan_kernel(const __grid_constant
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            if (on && i < each && first + i < p.NB) p.cnt[(size_t)(first + i) * p.E + e] = at;
+            if (on && i < each && first + i < p.NB) p.cnt[(size_t)(first + i) * p.pitch + e] = at;
             at += v[i];
         }
         carry += all;
@@ -587,29 +603,44 @@ __global__ void __launch_bounds__(1024) scored_scan_kernel(const __grid_constant
 }
 
 // Offsets and the places of one block's pairs.  scanned: cnt and total are those of
-// scored_scan_kernel; otherwise cnt holds the blocks' own counts, which every CTA adds up.
-__global__ void __launch_bounds__(SCAN_THREADS) scored_permute_kernel(const __grid_constant__ ScoredArgs p, int scanned) {
+// scored_scan_kernel; otherwise cnt holds the blocks' own counts, which every CTA adds up: four
+// experts a thread, the blocks dealt out to the strips of threads that the experts leave.
+__global__ void __launch_bounds__(SR_PERMUTE_THREADS) scored_permute_kernel(const __grid_constant__ ScoredArgs p, int scanned) {
     extern __shared__ __align__(16) uint8_t sr_smem[];
-    const int W = p.TB / 32;
-    int *base = reinterpret_cast<int *>(sr_smem), *before = base + p.E;   // [E] each
-    uint32_t *mask = reinterpret_cast<uint32_t *>(before + p.E);          // [E][W]
+    const int W = p.TB / 32, fours = p.pitch / 4, strips = SR_PERMUTE_THREADS / fours;
+    int *base = reinterpret_cast<int *>(sr_smem), *before = base + p.pitch;   // [pitch] each
+    int *sums = before + p.pitch;                                             // [2][strips][pitch]
+    uint32_t *mask = reinterpret_cast<uint32_t *>(sums + (scanned ? 0 : 2 * strips * p.pitch));   // [E][W]
     __shared__ int part[SCAN_THREADS / 32];
     const int t0 = blockIdx.x * p.TB, nt = min(p.TB, p.T - t0);
     for (int i = threadIdx.x; i < p.E * W; i += blockDim.x) mask[i] = p.mask[(size_t)blockIdx.x * p.E * W + i];
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-        if (scanned) {
+    if (scanned) {
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
             base[e] = p.total[e];
-            before[e] = p.cnt[(size_t)blockIdx.x * p.E + e];
-        } else {
-            int all = 0, mine = 0;
-#pragma unroll 32
-            for (int b = 0; b < p.NB; ++b) {
-                const int n = p.cnt[(size_t)b * p.E + e];
-                mine += b < blockIdx.x ? n : 0;
-                all += n;
+            before[e] = p.cnt[(size_t)blockIdx.x * p.pitch + e];
+        }
+    } else {
+        const int strip = threadIdx.x / fours, f = threadIdx.x - strip * fours;
+        if (strip < strips) {
+            int4 all = make_int4(0, 0, 0, 0), mine = make_int4(0, 0, 0, 0);
+#pragma unroll 8
+            for (int b = strip; b < p.NB; b += strips) {
+                const int4 n = *reinterpret_cast<const int4 *>(p.cnt + (size_t)b * p.pitch + 4 * f);
+                all.x += n.x; all.y += n.y; all.z += n.z; all.w += n.w;
+                if (b < blockIdx.x) { mine.x += n.x; mine.y += n.y; mine.z += n.z; mine.w += n.w; }
             }
-            base[e] = all;
-            before[e] = mine;
+            *reinterpret_cast<int4 *>(sums + strip * p.pitch + 4 * f) = all;
+            *reinterpret_cast<int4 *>(sums + (strips + strip) * p.pitch + 4 * f) = mine;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+            int a = 0, m = 0;
+            for (int i = 0; i < strips; ++i) {
+                a += sums[i * p.pitch + e];
+                m += sums[(strips + i) * p.pitch + e];
+            }
+            base[e] = a;
+            before[e] = m;
         }
     }
     __syncthreads();

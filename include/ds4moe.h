@@ -288,7 +288,7 @@ size_t ds4moe_route_logits_workspace(const ds4moe_router *r, int32_t T);
  *  four pointers may be NULL.  expert_offsets_dev [E+1] counts placed pairs only; entries of
  *  sorted_token_dev / sorted_slot_dev [T*k] from expert_offsets_dev[E] on are left as they
  *  were; inv_pos_dev [T*k] is -1 for a slot without an expert.  T = 0 zeroes the offsets.
- *  workspace_dev: at least ds4moe_route_logits_workspace bytes, 4-byte aligned, needed when
+ *  workspace_dev: at least ds4moe_route_logits_workspace bytes, 16-byte aligned, needed when
  *  that is not 0 and a permutation output is given; its contents do not matter.  Two calls
  *  (or captured graphs) that may run at the same time need a workspace each. */
 ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev, int32_t logits_type, int64_t ld,
