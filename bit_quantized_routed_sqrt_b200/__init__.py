@@ -203,56 +203,58 @@ def ds4moe_mxfp4_last_error(handle) -> str:
     return lib.ds4moe_mxfp4_last_error(handle).decode()
 
 
-_TYPES = {"torch.float32": F32, "torch.bfloat16": BF16, "torch.float16": F16}
-_type_codes = {}
+_torch = None
+_types, _dtypes = {}, {}
+_raw_stream = _current_device = None
+
+
+def _bind_torch():
+    """What the functions below take from torch, looked up once."""
+    global _torch, _raw_stream, _current_device
+    import torch
+    _types.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+    _dtypes.update(int32=torch.int32, uint8=torch.uint8, float32=torch.float32)
+    # the address of a device's current stream without a Stream object (3 us a call less)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _torch = torch
 
 
 def _type_of(t, what: str) -> int:
-    c = _type_codes.get(t.dtype)
-    if c is None:
-        c = _type_codes[t.dtype] = _TYPES.get(str(t.dtype), -1)
-    if c < 0:
+    code = _types.get(t.dtype)
+    if code is None:
         raise ValueError("%s must be float32, bfloat16 or float16, not %s" % (what, t.dtype))
-    return c
+    return code
 
 
 def _rows_of(t, what: str):
     """(rows, width, elements between rows) of a matrix whose rows are contiguous."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("%s must have two dimensions" % what)
-    rows, width = t.shape
-    ld = t.stride(0) if rows > 1 else width
-    if (width > 1 and t.stride(1) != 1) or ld < width:
+    rows, width = shape
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = width
+    if (width > 1 and step != 1) or ld < width:
         raise ValueError("%s must have contiguous rows, one behind the other" % what)
     return rows, width, ld
 
 
 def _flat(t, dtype: str, n: int, what: str, device):
-    """t as a contiguous tensor of n elements of the type on the device (None stays None)."""
+    """The address of a contiguous tensor of n elements of the type on the device (None stays None)."""
     if t is None:
         return None
-    if t.dtype is not _torch_dtypes()[dtype] or t.numel() != n or not t.is_contiguous() or t.device != device:
+    if t.dtype is not _dtypes[dtype] or t.numel() != n or not t.is_contiguous() or t.device != device:
         raise ValueError("%s must be a contiguous %s tensor of %d elements on %s" % (what, dtype, n, device))
-    return t
-
-
-_dtypes = {}
-_raw_stream = None
-
-
-def _torch_dtypes():
-    global _raw_stream
-    if not _dtypes:
-        import torch
-        _dtypes.update(int32=torch.int32, uint8=torch.uint8, float32=torch.float32)
-        # the address of a device's current stream without a Stream object (3 us a call less)
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return _dtypes
+    return t.data_ptr()
 
 
 def _device_of(t, what: str):
     """The tensor's CUDA device."""
+    if _torch is None:
+        _bind_torch()
     if not t.is_cuda:
         raise ValueError("%s must be on a CUDA device" % what)
     return t.device
@@ -260,21 +262,20 @@ def _device_of(t, what: str):
 
 def _run(device, call, *args):
     """call(*args, stream) on the device and its current stream; the current device is the same afterwards."""
-    import torch
-    _torch_dtypes()
     index = device.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         return call(*args, _raw_stream(index))
-    with torch.cuda.device(index):
+    with _torch.cuda.device(index):
         return call(*args, _raw_stream(index))
-
-
-def _addr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
 
 
 class Routing:
-    """Outputs and workspace of Router.route for T tokens (Router.buffers)."""
+    """Outputs and workspace of Router.route for T tokens (Router.buffers); its tensors stay the same."""
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "addresses"):
+            raise AttributeError("the buffers of a Routing are fixed")
+        object.__setattr__(self, name, value)
 
     def __init__(self, router: "Router", T: int, device):
         import torch
@@ -289,11 +290,9 @@ class Routing:
         n = ds4moe_route_logits_workspace(router.cfg, T)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
-    @property
-    def addresses(self):
-        return (self.topk_idx.data_ptr(), self.topk_w.data_ptr(), self.expert_offsets.data_ptr(),
-                self.sorted_token.data_ptr(), self.sorted_slot.data_ptr(), self.inv_pos.data_ptr(),
-                _addr(self.workspace), 0 if self.workspace is None else self.workspace.numel())
+        self.addresses = (self.topk_idx.data_ptr(), self.topk_w.data_ptr(), self.expert_offsets.data_ptr(),
+                          self.sorted_token.data_ptr(), self.sorted_slot.data_ptr(), self.inv_pos.data_ptr(),
+                          self.workspace.data_ptr() if n else None, n)
 
 
 class Router:
@@ -311,88 +310,81 @@ class Router:
 
     def route(self, logits, bias=None, out: Optional[Routing] = None) -> Routing:
         """Routes the rows of logits [T, E] (rows may be strided); out: buffers of T tokens to write to."""
-        T, E, ld = _rows_of(logits, "logits")
         device = _device_of(logits, "logits")
+        T, E, ld = _rows_of(logits, "logits")
         code = _type_of(logits, "logits")
         if E != self.cfg.n_experts:
             raise ValueError("logits have %d columns for %d experts" % (E, self.cfg.n_experts))
-        _flat(bias, "float32", E, "bias", device)
+        bias_at = _flat(bias, "float32", E, "bias", device)   # bias itself stays alive to the call
         if out is None:
             out = Routing(self, T, device)
         elif out.size != (T, self.cfg.top_k, E) or out.topk_idx.device != device:
             raise ValueError("out holds buffers of another size or device")
-        _check(_run(device, lib.ds4moe_route_logits, C.byref(self.cfg), logits.data_ptr(), code, ld,
-                    T, _addr(bias), *out.addresses), None, "ds4moe_route_logits")
+        _check(_run(device, lib.ds4moe_route_logits, C.byref(self.cfg), logits.data_ptr(), code, ld, T, bias_at,
+                    *out.addresses), None, "ds4moe_route_logits")
         return out
 
 
 def mxfp4_quantize(x, inv_pos=None, codes=None, scales=None):
     """(codes, scales) of the rows of x; with inv_pos [rows, k] (int32) row r goes to rows inv_pos[r, j]
     of codes / scales (rows * k of them where they are not given)."""
-    rows, K, ld = _rows_of(x, "x")
     device = _device_of(x, "x")
+    rows, K, ld = _rows_of(x, "x")
     code = _type_of(x, "x")
     if K == 0 or K % 32:
         raise ValueError("the rows of x must have a multiple of 32 elements")
-    k = 1
+    k, places = 1, None
     if inv_pos is not None:
         if inv_pos.dim() != 2 or inv_pos.shape[0] != rows:
             raise ValueError("inv_pos must have a row for each row of x")
         k = inv_pos.shape[1]
-        _flat(inv_pos, "int32", rows * k, "inv_pos", device)
+        places = _flat(inv_pos, "int32", rows * k, "inv_pos", device)
     if codes is None:
-        import torch
-        codes = torch.empty((rows * k, K // 2), dtype=torch.uint8, device=x.device)
+        codes = _torch.empty((rows * k, K // 2), dtype=_torch.uint8, device=device)
     out_rows = codes.shape[0]
     if scales is None:
-        import torch
-        scales = torch.empty((out_rows, K // 32), dtype=torch.uint8, device=x.device)
-    _flat(codes, "uint8", out_rows * (K // 2), "codes", device)
-    _flat(scales, "uint8", out_rows * (K // 32), "scales", device)
-    _check(_run(device, lib.ds4moe_mxfp4_quantize, x.data_ptr(), code, ld, rows, K, _addr(inv_pos),
-                k, out_rows, codes.data_ptr(), scales.data_ptr()), None, "ds4moe_mxfp4_quantize")
+        scales = _torch.empty((out_rows, K // 32), dtype=_torch.uint8, device=device)
+    _check(_run(device, lib.ds4moe_mxfp4_quantize, x.data_ptr(), code, ld, rows, K, places, k, out_rows,
+                _flat(codes, "uint8", out_rows * (K // 2), "codes", device),
+                _flat(scales, "uint8", out_rows * (K // 32), "scales", device)), None, "ds4moe_mxfp4_quantize")
     return codes, scales
 
 
 def mxfp4_dequantize(codes, scales, out=None):
     """The values of MXFP4 rows, in out (float32, bfloat16 or float16 [rows, K]; bfloat16 where it is not given,
     which holds every value but 2^-127 * 0.5 exactly)."""
+    device = _device_of(codes, "codes")
     rows, half, _ = _rows_of(codes, "codes")
     K = 2 * half
-    device = _device_of(codes, "codes")
-    _flat(codes, "uint8", rows * half, "codes", device)
-    _flat(scales, "uint8", rows * (K // 32), "scales", device)
     if out is None:
-        import torch
-        out = torch.empty((rows, K), dtype=torch.bfloat16, device=codes.device)
+        out = _torch.empty((rows, K), dtype=_torch.bfloat16, device=device)
     r, w, ld = _rows_of(out, "out")
-    if (r, w) != (rows, K) or out.device != device:
+    if r != rows or w != K or out.device != device:
         raise ValueError("out must be [%d, %d] on %s" % (rows, K, device))
-    _check(_run(device, lib.ds4moe_mxfp4_dequantize, codes.data_ptr(), scales.data_ptr(), rows, K,
-                out.data_ptr(), _type_of(out, "out"), ld), None, "ds4moe_mxfp4_dequantize")
+    _check(_run(device, lib.ds4moe_mxfp4_dequantize, _flat(codes, "uint8", rows * half, "codes", device),
+                _flat(scales, "uint8", rows * (K // 32), "scales", device), rows, K, out.data_ptr(), _type_of(out, "out"),
+                ld), None, "ds4moe_mxfp4_dequantize")
     return out
 
 
 def combine(o, inv_pos, topk_w, y=None, add=None):
     """y[t] = add[t] + sum_j topk_w[t, j] * o[inv_pos[t, j]] (a row outside o adds nothing); y is float32 where it
     is not given."""
-    o_rows, H, ld = _rows_of(o, "o")
     device = _device_of(o, "o")
+    o_rows, H, ld = _rows_of(o, "o")
     if ld != H:
         raise ValueError("o must be contiguous")
     if topk_w.dim() != 2:
         raise ValueError("topk_w must be [T, k]")
     T, k = topk_w.shape
-    _flat(topk_w, "float32", T * k, "topk_w", device)
-    _flat(inv_pos, "int32", T * k, "inv_pos", device)
     if y is None:
-        import torch
-        y = torch.empty((T, H), dtype=torch.float32, device=o.device)
+        y = _torch.empty((T, H), dtype=_torch.float32, device=device)
     for t, what in ((y, "y"), (add, "add")):
         if t is not None and (t.shape != (T, H) or not t.is_contiguous() or t.device != device):
             raise ValueError("%s must be a contiguous [%d, %d] tensor on %s" % (what, T, H, device))
     _check(_run(device, lib.ds4moe_combine, o.data_ptr(), _type_of(o, "o"), o_rows, T, k, H,
-                inv_pos.data_ptr(), topk_w.data_ptr(), _addr(add), 0 if add is None else _type_of(add, "add"), y.data_ptr(),
+                _flat(inv_pos, "int32", T * k, "inv_pos", device), _flat(topk_w, "float32", T * k, "topk_w", device),
+                None if add is None else add.data_ptr(), F32 if add is None else _type_of(add, "add"), y.data_ptr(),
                 _type_of(y, "y")), None, "ds4moe_combine")
     return y
 
@@ -434,37 +426,33 @@ class Mxfp4Experts:
             raise ValueError("a gated projection takes two matrices, another takes one")
         device = self._device_of(codes, "codes")
         n = self.n_experts * self.n_out
-        for t, per, what in ((codes, self.n_in // 2, "codes"), (scales, self.n_in // 32, "scales"),
-                             (up_codes, self.n_in // 2, "up_codes"), (up_scales, self.n_in // 32, "up_scales")):
-            _flat(t, "uint8", n * per, what, device)
-        _check_mxfp4(_run(device, lib.ds4moe_mxfp4_load, self.h, codes.data_ptr(), scales.data_ptr(),
-                          _addr(up_codes), _addr(up_scales)), self.h, "ds4moe_mxfp4_load")
+        _check_mxfp4(_run(device, lib.ds4moe_mxfp4_load, self.h,
+                          _flat(codes, "uint8", n * (self.n_in // 2), "codes", device),
+                          _flat(scales, "uint8", n * (self.n_in // 32), "scales", device),
+                          _flat(up_codes, "uint8", n * (self.n_in // 2), "up_codes", device),
+                          _flat(up_scales, "uint8", n * (self.n_in // 32), "up_scales", device)), self.h, "ds4moe_mxfp4_load")
 
     def product(self, a_codes, a_scales, offsets=None, out=None, out_scales=None):
         """Rows of a [rows, n_in] in MXFP4, grouped by offsets int32 [E + 1] (None for one expert), times their
         experts' matrices.  out: [rows, n_out] of float32, bfloat16 (where it is not given) or float16, rows may be
         strided; or uint8 [rows, n_out / 2] with out_scales uint8 [rows, n_out / 32] for MXFP4."""
-        rows, half, _ = _rows_of(a_codes, "a_codes")
         device = self._device_of(a_codes, "a_codes")
+        rows, half, _ = _rows_of(a_codes, "a_codes")
         if half * 2 != self.n_in:
             raise ValueError("a_codes has rows of %d inputs, the experts take %d" % (half * 2, self.n_in))
-        _flat(a_codes, "uint8", rows * half, "a_codes", device)
-        _flat(a_scales, "uint8", rows * (self.n_in // 32), "a_scales", device)
-        _flat(offsets, "int32", self.n_experts + 1, "offsets", device)
         if out is None:
-            import torch
-            out = torch.empty((rows, self.n_out), dtype=torch.bfloat16, device=a_codes.device)
+            out = _torch.empty((rows, self.n_out), dtype=_torch.bfloat16, device=device)
         if out_scales is not None:
-            _flat(out, "uint8", rows * (self.n_out // 2), "out", device)
-            _flat(out_scales, "uint8", rows * (self.n_out // 32), "out_scales", device)
-            code, ld = MXFP4, self.n_out
+            to, ld, code = _flat(out, "uint8", rows * (self.n_out // 2), "out", device), self.n_out, MXFP4
         else:
             r, n, ld = _rows_of(out, "out")
-            if (r, n) != (rows, self.n_out) or out.device != device:
+            if r != rows or n != self.n_out or out.device != device:
                 raise ValueError("out must be [%d, %d] on %s" % (rows, self.n_out, device))
-            code = _type_of(out, "out")
-        _check_mxfp4(_run(device, lib.ds4moe_mxfp4_product, self.h, a_codes.data_ptr(),
-                          a_scales.data_ptr(), rows, _addr(offsets), out.data_ptr(), code, ld, _addr(out_scales)), self.h,
+            to, code = out.data_ptr(), _type_of(out, "out")
+        _check_mxfp4(_run(device, lib.ds4moe_mxfp4_product, self.h, _flat(a_codes, "uint8", rows * half, "a_codes", device),
+                          _flat(a_scales, "uint8", rows * (self.n_in // 32), "a_scales", device), rows,
+                          _flat(offsets, "int32", self.n_experts + 1, "offsets", device), to, code, ld,
+                          _flat(out_scales, "uint8", rows * (self.n_out // 32), "out_scales", device)), self.h,
                      "ds4moe_mxfp4_product")
         return out
 
