@@ -27,13 +27,17 @@ __device__ __forceinline__ void mx_group(const MxArgs &p, int e, int &first, int
 }
 
 // ------------------------------------------------------------------ tcgen05
+// out[r][n] = sum_k a[r][k] W[n][k] over each expert's rows: products of two E2M1 values and two
+// powers of two are exact, the sums are fp32.  The weights bound it where an expert has few rows
+// (17/32 byte a weight: 6.3 TB/s at 128 rows of 256 experts, 97% of a copy's rate), the steps of
+// the ring below where it has many (3.6 PFLOP/s at 8191 x 4096 x 4096).
+//
 // A persistent kernel, one CTA per SM, over tiles of 128 packed weight rows (the MMA's M) x up
 // to NT rows of a (the MMA's N): each expert's rows are cut into equal tiles of at most NT, and
 // the tiles that share weight rows follow one another, so the weights cross HBM once.  One
 // K step is 256 inputs: a weight tile with its scales (one contiguous bulk copy), the rows'
-// codes (TMA, 128-byte swizzle) and the rows'
-// scales, then four block-scaled MMAs of 64 inputs (kind::mxf4, E2M1 x E2M1 with an E8M0 scale
-// per 32, exact products, fp32 accumulators in tensor memory).
+// codes (TMA, 128-byte swizzle) and the rows' scales, then four block-scaled MMAs of 64 inputs
+// (kind::mxf4: E2M1 x E2M1 with an E8M0 scale per 32, fp32 accumulators in tensor memory).
 //   warps 0, 3 producers of weight tiles and of row codes
 //   warp 1     allocates tensor memory; copies the step's scales there (tcgen05.cp) and issues
 //              the MMAs.  Every stage has its own scale columns, so a copy never meets an MMA
@@ -42,12 +46,17 @@ __device__ __forceinline__ void mx_group(const MxArgs &p, int e, int &first, int
 //              memory as the copy wants them
 //   warps 4-11 epilogue, in two groups of four that take chunks of 32 rows in turn: accumulators
 //              -> silu(g) * u -> output.  A lane is an output, so a warp stores 32 (gated: two
-//              times 16) neighbouring elements of a row at once; staging 128-byte rows in shared
-//              memory with four warps kept the tensor pipe waiting (1.13 ms against XXX at 65536
-//              rows x 7168 x 2048)
+//              times 16) neighbouring elements of a row at once: 740 cycles a chunk, where a store
+//              under a test of its row each took 3000 and made the epilogue the bound (1.06 against
+//              0.95 ms at 65536 rows x 7168 x 2048)
 // The accumulators are double buffered, so a tile's epilogue overlaps the next tile.
 // Every wait is bounded, as in the layer's grouped GEMM: on a timeout the CTA records
 // ETIMEOUT, waits for its own copies and MMAs, frees tensor memory and returns.
+//
+// What a step costs beside its MMAs (130 to 510 cycles) is the roles' serial work: a successful
+// barrier test takes 150 cycles, the issue of a bulk copy 55 and of a TMA load 100 more.  Pairs
+// of CTAs (cta_group::2, half the rows' traffic) measured 5% faster at 8191 x 4096 x 4096 and 7%
+// slower at 65536 x 7168 x 2048; two steps at a time in the MMA warp 8% slower at both.
 constexpr int MX_THREADS = 416;
 constexpr int MX_CHUNK = 32;             // rows of a (accumulator columns) that an epilogue warp takes at a time
 // MXFP4 output: of each pair of epilogue warps, two buffers of the codes of 32 rows x 32
@@ -55,9 +64,8 @@ constexpr int MX_CHUNK = 32;             // rows of a (accumulator columns) that
 constexpr int MX_PAIR_BYTES = 2 * (32 * 16 + 2 * 32);
 
 // BOX1 < BOX0 < NT: the row counts that one TMA load can bring (a tile takes the least that holds it).
-template <int NT_, int BOX0_, int BOX1_, int STAGES_, int CTAS_, bool GATED_>
+template <int NT_, int BOX0_, int BOX1_, int STAGES_, bool GATED_>
 struct MxCfg {
-    static constexpr int CTAS = CTAS_;   // a SM
     static constexpr int NT = NT_, BOX0 = BOX0_, BOX1 = BOX1_, STAGES = STAGES_;
     static constexpr bool GATED = GATED_;
     static constexpr int SF_CHUNKS = (NT + 127) / 128;                 // 512-byte scale chunks of the rows per 128 inputs
@@ -76,7 +84,7 @@ struct MxCfg {
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES + S_BYTES;
     static_assert(COLS <= 512, "tensor memory");
     static_assert(STAGES >= 4, "a scale warp waits on every other pair of steps, at most 3 steps apart");
-    static_assert(CTAS * (SMEM + 1024) <= 228 * 1024 && CTAS * TMEM <= 512, "shared and tensor memory of a SM");
+    static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
     static_assert(NT % 16 == 0 && NT > BOX0 && BOX0 > BOX1 && BOX1 % 8 == 0, "row tiles");
     static_assert((2 * STAGES + 5) * 8 + 16 + 32 + 4 * STAGES <= BAR_BYTES, "barrier area");
 };
@@ -261,17 +269,17 @@ __device__ __forceinline__ void mx_store_chunk_mxfp4(const MxArgs &p, const floa
 }
 
 template <class C>
-__global__ void __launch_bounds__(MX_THREADS, C::CTAS)
+__global__ void __launch_bounds__(MX_THREADS, 1)
     mxfp4_product_kernel(const __grid_constant__ CUtensorMap tm_nt, const __grid_constant__ CUtensorMap tm_box0,
                          const __grid_constant__ CUtensorMap tm_box1, const __grid_constant__ MxArgs p) {
     extern __shared__ __align__(1024) uint8_t mx_smem_raw[];
     uint8_t *stages = mx_smem_raw + ((1024u - (smem_u32(mx_smem_raw) & 1023u)) & 1023u);
     uint8_t *epi = stages + C::STAGES * C::STAGE_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(epi + C::EPI_BYTES);
-    uint64_t *full = bars;                       // [S] two producers (with their bytes) and the scale warp
+    uint64_t *full = bars;                       // [S] two producers (with their bytes) and a scale warp
     uint64_t *empty = full + C::STAGES;          // [S] MMA commit
     uint64_t *acc_full = empty + C::STAGES;      // [2] MMA commit
-    uint64_t *acc_empty = acc_full + 2;          // [2] 4 epilogue warps
+    uint64_t *acc_empty = acc_full + 2;          // [2] 8 epilogue warps
     uint64_t *drain = acc_empty + 2;             // MMA commit at exit
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(drain + 2);

@@ -34,8 +34,8 @@
  *  - Test hook: the environment variable DS4MOE_FAULT injects a host-side failure without
  *    touching the GPU: "alloc" (ds4moe_create returns DS4MOE_ENOMEM), "h2d"
  *    (ds4moe_load_q2k_experts returns DS4MOE_ECUDA before its first copy), "launch"
- *    (ds4moe_route / ds4moe_route_static / ds4moe_forward return DS4MOE_ECUDA before their
- *    first launch).  It is read on every call.
+ *    (ds4moe_route / ds4moe_route_static / ds4moe_forward and the operators beside the layer
+ *    return DS4MOE_ECUDA before their first launch).  It is read on every call.
  */
 #ifndef DS4MOE_H
 #define DS4MOE_H
@@ -302,8 +302,8 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
  * block with a NaN or an infinity gets scale byte 255 (NaN).
  *  inv_pos_dev NULL: row r -> row r (out_rows >= rows).  Otherwise inv_pos_dev [rows][top_k]
  *  and row r -> rows inv_pos[r][j], j < top_k (1 .. 32); entries outside [0, out_rows) are
- *  skipped, so the rows of tokens land in expert order.  Rows that are no target are left as
- *  they were.  codes_dev [out_rows][K/2] (16-byte aligned), scales_dev [out_rows][K/32]. */
+ *  skipped, so the rows of tokens land in expert order.  No row may be named twice.  Rows that
+ *  are no target are left as they were.  codes_dev [out_rows][K/2] (16-byte aligned), scales_dev [out_rows][K/32]. */
 ds4moe_status ds4moe_mxfp4_quantize(const void *x_dev, int32_t x_type, int64_t ld, int32_t rows, int32_t K,
                                     const int32_t *inv_pos_dev, int32_t top_k, int32_t out_rows, uint8_t *codes_dev,
                                     uint8_t *scales_dev, void *cuda_stream);
@@ -346,7 +346,9 @@ ds4moe_status ds4moe_mxfp4_load(ds4moe_mxfp4 *h, const uint8_t *codes_dev, const
  * (N % 32 == 0, ld == N) is quantised as by ds4moe_mxfp4_quantize into out_dev [rows][N/2]
  * (16-byte aligned) and out_scales_dev [rows][N/32] (NULL for the other types).  Rows behind
  * expert_offsets_dev[E] are neither used nor written.  Products whose magnitude is below the
- * normal range of fp32 may count as zero. */
+ * normal range of fp32 may count as zero.  Offsets do not decrease; rows they claim beyond
+ * `rows` do not count.  Calls of one handle may overlap on the device (it has no workspace),
+ * but not with ds4moe_mxfp4_load. */
 ds4moe_status ds4moe_mxfp4_product(ds4moe_mxfp4 *h, const uint8_t *a_codes_dev, const uint8_t *a_scales_dev, int32_t rows,
                                    const int32_t *expert_offsets_dev, void *out_dev, int32_t out_type, int64_t ld,
                                    uint8_t *out_scales_dev, void *cuda_stream);

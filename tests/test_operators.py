@@ -517,6 +517,76 @@ def test_combine_in_place(ds4):
     assert torch.equal(add, want)
 
 
+# ------------------------------------------------------------------ unaligned and far places
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("E", [128, 256, 512])
+def test_route_rows_that_are_not_aligned_pieces(ds4, kind, E):
+    wide = torch.randn(20, E + 5, generator=gen(E)).to(TYPES[kind]).cuda()
+    check_route(ds4, wide[:, 2:2 + E], 8, score="sigmoid")
+    check_route(ds4, wide[:, 2:2 + E], 8, torch.randn(E, generator=gen(1)) * 0.1, score="softmax", n_groups=8, topk_groups=3)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("H", [1, 7, 33, 96, 1021, 2050])
+@pytest.mark.parametrize("first", [0, 1, 3])
+def test_combine_rows_at_any_element(ds4, kind, H, first):
+    g = gen(H)
+    T, k = 9, 5
+    o = torch.randn(T * k + 4, H, generator=g).to(TYPES[kind]).cuda()[first:first + T * k]
+    inv = torch.randperm(T * k, generator=g).int().reshape(T, k)
+    w = torch.rand(T, k, generator=g)
+    add = torch.randn(T + 1, H, generator=g).cuda()[1:]
+    y = torch.full((T + 2, H), 77.0, device="cuda")
+    ds4.combine(o, inv.cuda(), w.cuda(), y[1:T + 1], add)
+    terms = o.double().cpu().numpy()[inv.numpy()] * w.double().numpy()[:, :, None]
+    want, size = terms.sum(1) + add.double().cpu().numpy(), np.abs(terms).sum(1) + np.abs(add.double().cpu().numpy())
+    tol = (k + 1) * ref.U24 * size + np.abs(want) * ref.U24
+    assert (np.abs(y[1:T + 1].double().cpu().numpy() - want) <= tol).all()
+    assert (y[0] == 77).all() and (y[T + 1] == 77).all()
+
+
+@pytest.mark.parametrize("K", [64, 512, 1024])
+@pytest.mark.parametrize("shift", [1, 2, 4, 7])
+def test_product_scales_at_any_byte(ds4, K, shift):
+    ex, mats = make(ds4, 2, 96, K, False, 40)
+    codes, scales = mx_random((30, K), gen(41))
+    held = torch.zeros(scales.numel() + 16, dtype=torch.uint8, device="cuda")
+    held[shift:shift + scales.numel()] = scales.reshape(-1).cuda()
+    off = offsets_of([11, 19])
+    out = ex.product(codes.cuda(), held[shift:shift + scales.numel()].view(30, K // 32), off.cuda(), torch.empty(30, 96, device="cuda"))
+    want, bound = ref.product(values(codes, scales), mats, off.numpy())
+    assert (np.abs(out.double().cpu().numpy() - want) <= bound + np.abs(want) * ref.U24).all()
+
+
+def test_rows_far_apart(ds4):
+    """Row strides of 2^30 + 32 elements: offsets beyond 32 bits, of elements and of bytes."""
+    far = (1 << 30) + 32
+    g = gen(50)
+    held = torch.zeros(4 * far + 4096, dtype=torch.bfloat16, device="cuda")
+    view = held.as_strided((5, 256), (far, 1))
+    x = torch.randn(5, 256, generator=g).bfloat16()
+    view.copy_(x.cuda())
+    codes, scales = ds4.mxfp4_quantize(view)
+    c, s = ref.quantize(x.double().numpy())
+    assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), s)
+    check_route(ds4, view, 8, score="sigmoid")
+    held.zero_()
+    ds4.mxfp4_dequantize(codes, scales, view)
+    assert torch.equal(view.cpu().double(), torch.from_numpy(ref.dequantize(c, s)))
+    ex, mats = make(ds4, 1, 256, 256, False, 51)
+    ex.product(codes, scales, None, view)
+    want, bound = ref.product(ref.dequantize(c, s), mats, [0, 5])
+    assert (np.abs(view.double().cpu().numpy() - want) <= bound + (np.abs(want) + bound) * 2.0 ** -8).all()
+    del view, held
+    # rows of o beyond 2^31 elements
+    H, rows = 1 << 20, 2200
+    o = torch.zeros(rows, H, dtype=torch.bfloat16, device="cuda")
+    o[rows - 1], o[rows - 2, 5] = 3.0, 1.0
+    inv = torch.tensor([[rows - 1, 0], [rows - 2, rows]], dtype=torch.int32).cuda()
+    y = ds4.combine(o, inv, torch.tensor([[0.5, 1.0], [2.0, 1.0]]).cuda())
+    assert (y[0] == 1.5).all() and y[1, 5] == 2.0 and y[1].sum() == 2.0
+
+
 # ------------------------------------------------------------------ together
 class Chain:
     """An MoE FFN of MXFP4 experts as a program runs it, every buffer its own."""
