@@ -37,7 +37,8 @@ __device__ __forceinline__ void mx_group(const MxArgs &p, int e, int &first, int
 // the tiles that share weight rows follow one another, so the weights cross HBM once.  One
 // K step is 256 inputs: a weight tile with its scales (one contiguous bulk copy), the rows'
 // codes (TMA, 128-byte swizzle) and the rows' scales, then four block-scaled MMAs of 64 inputs
-// (kind::mxf4: E2M1 x E2M1 with an E8M0 scale per 32, fp32 accumulators in tensor memory).
+// (kind::mxf4: E2M1 x E2M1 with an E8M0 scale per 32, fp32 accumulators in tensor memory).  A
+// stage of the ring holds one or two such steps.
 //   warps 0, 3 producers of weight tiles and of row codes
 //   warp 1     allocates tensor memory; copies the step's scales there (tcgen05.cp) and issues
 //              the MMAs.  Every stage has its own scale columns, so a copy never meets an MMA
@@ -64,17 +65,21 @@ constexpr int MX_CHUNK = 32;             // rows of a (accumulator columns) that
 constexpr int MX_PAIR_BYTES = 2 * (32 * 16 + 2 * 32);
 
 // BOX1 < BOX0 < NT: the row counts that one TMA load can bring (a tile takes the least that holds it).
-template <int NT_, int BOX0_, int BOX1_, int STAGES_, bool GATED_>
+// PER: input tiles (of 256) a stage.
+template <int NT_, int BOX0_, int BOX1_, int STAGES_, int PER_, bool GATED_>
 struct MxCfg {
+    static constexpr int PER = PER_;
     static constexpr int NT = NT_, BOX0 = BOX0_, BOX1 = BOX1_, STAGES = STAGES_;
     static constexpr bool GATED = GATED_;
     static constexpr int SF_CHUNKS = (NT + 127) / 128;                 // 512-byte scale chunks of the rows per 128 inputs
     static constexpr int B_BYTES = (NT * 128 + 1023) / 1024 * 1024;
     static constexpr int SFB_BYTES = 2 * SF_CHUNKS * 512;
-    // weight codes | weight scales | row scales | (to 1024) | row codes
-    static constexpr int B_OFF = (MX_TILE_BYTES + SFB_BYTES + 1023) / 1024 * 1024;
-    static constexpr int STAGE_BYTES = B_OFF + B_BYTES;
-    static constexpr int SF_COLS = 8 + 8 * SF_CHUNKS;                  // tensor memory columns of a stage's scales
+    // PER of each: weight tiles (codes, scales) | row scales | (to 1024) | row codes
+    static constexpr int SFB_OFF = PER * MX_TILE_BYTES;
+    static constexpr int B_OFF = (SFB_OFF + PER * SFB_BYTES + 1023) / 1024 * 1024;
+    static constexpr int STAGE_BYTES = B_OFF + PER * B_BYTES;
+    static constexpr int TILE_COLS = 8 + 8 * SF_CHUNKS;                // tensor memory columns of an input tile's scales
+    static constexpr int SF_COLS = PER * TILE_COLS;                    // and of a stage's
     static constexpr int COLS = 2 * NT + STAGES * SF_COLS;
     static constexpr int TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static constexpr int F = GATED ? 64 : 128;                         // outputs of a tile
@@ -83,7 +88,7 @@ struct MxCfg {
     static constexpr int S_BYTES = 3 * (SR_MAX_EXPERTS + 1) * 4;
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES + S_BYTES;
     static_assert(COLS <= 512, "tensor memory");
-    static_assert(STAGES >= 4, "a scale warp waits on every other pair of steps, at most 3 steps apart");
+    static_assert(PER <= 2 && STAGES * PER >= 4, "a scale warp waits on every other pair of input tiles");
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
     static_assert(NT % 16 == 0 && NT > BOX0 && BOX0 > BOX1 && BOX1 % 8 == 0, "row tiles");
     static_assert((2 * STAGES + 5) * 8 + 16 + 32 + 4 * STAGES <= BAR_BYTES, "barrier area");
@@ -110,7 +115,7 @@ __device__ __forceinline__ void mx_copy_scales(uint32_t tmem, uint32_t smem) {
 }
 
 // Flags beside the rows of a step's tile.
-constexpr uint32_t MX_FIRST = 1u << 30, MX_LAST = 1u << 31;
+constexpr uint32_t MX_HALF = 1u << 29, MX_FIRST = 1u << 30, MX_LAST = 1u << 31;   // half: one input tile
 
 // Whether the phase of that parity has completed, without waiting.
 __device__ __forceinline__ uint32_t mx_test(uint32_t bar, uint32_t parity) {
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
     __syncthreads();
 
     const int packed_rows = C::GATED ? 2 * p.N : p.N;
-    const int MT = (packed_rows + MX_TM - 1) / MX_TM, KT = (p.K + MX_TK - 1) / MX_TK;
+    const int MT = (packed_rows + MX_TM - 1) / MX_TM, KT = (p.K + MX_TK - 1) / MX_TK, KS = (KT + C::PER - 1) / C::PER;
     const uint32_t tiles = (uint32_t)units * MT;
     MxTiles<C::NT> walk(S, p.E, MT, tiles);
 
@@ -338,15 +343,22 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
             const uint8_t *w = p.w + (size_t)x.e * p.expert_bytes + (size_t)x.m * KT * MX_TILE_BYTES;
             const CUtensorMap *map = x.n <= C::BOX1 ? &tm_box1 : x.n <= C::BOX0 ? &tm_box0 : &tm_nt;
             const uint32_t bytes = weights ? MX_TILE_BYTES : 128 * (x.n <= C::BOX1 ? C::BOX1 : x.n <= C::BOX0 ? C::BOX0 : C::NT);
-            for (int kt = 0; kt < KT; ++kt, ++it) {
+            for (int ks = 0; ks < KS; ++ks, ++it) {
                 const uint32_t s = it % C::STAGES;
                 if (!(ok = mbar_wait(smem_u32(empty + s), ((it / C::STAGES) & 1) ^ 1, abort, p.status))) break;
+                const bool half = C::PER == 2 && 2 * ks + 1 == KT;
                 if (elect_one()) {
                     const uint32_t st = smem_u32(stages + s * C::STAGE_BYTES), bar = smem_u32(full + s);
-                    if (!weights) meta[s] = x.n | (kt == 0 ? MX_FIRST : 0u) | (kt == KT - 1 ? MX_LAST : 0u);
-                    mbar_expect_tx(bar, bytes);   // releases meta to the MMA warp
-                    if (weights) bulk_g2s(st, w + (size_t)kt * MX_TILE_BYTES, MX_TILE_BYTES, bar);
-                    else tma_load_2d(st + C::B_OFF, map, kt * (MX_TK / 2), x.row0, bar);
+                    if (!weights)
+                        meta[s] = x.n | (ks == 0 ? MX_FIRST : 0u) | (ks == KS - 1 ? MX_LAST : 0u) | (half ? MX_HALF : 0u);
+                    mbar_expect_tx(bar, half ? bytes : C::PER * bytes);   // releases meta to the MMA warp
+                    if (weights) {
+                        bulk_g2s(st, w + (size_t)ks * C::PER * MX_TILE_BYTES, half ? bytes : C::PER * bytes, bar);
+                    } else {
+                        tma_load_2d(st + C::B_OFF, map, ks * C::PER * (MX_TK / 2), x.row0, bar);
+                        if (C::PER == 2 && !half)
+                            tma_load_2d(st + C::B_OFF + C::B_BYTES, map, ks * MX_TK + MX_TK / 2, x.row0, bar);
+                    }
                 }
                 __syncwarp();
             }
@@ -360,7 +372,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         // the next stage's barrier is asked before this step's MMAs are issued, so that this
         // warp, the one that bounds a step, neither walks the tiles (700 cycles each) nor waits
         // out the 150 cycles of a successful barrier test.
-        const uint32_t mine = walk.more() ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0, total = mine * (uint32_t)KT;
+        const uint32_t mine = walk.more() ? (tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0, total = mine * (uint32_t)KS;
         uint32_t tc = 0, idesc0 = 0, idesc2 = 0, d = tmem, b = 0;
         bool ok = true, ready = false;
         for (uint32_t it = 0; it < total; ++it) {
@@ -381,21 +393,27 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
             const uint32_t sfa = tmem + 2 * C::NT + s * C::SF_COLS, sfb = sfa + 8;
             const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + C::B_OFF);
             if (elect_one()) {
-                // Unrolled, with every operand a constant off the step's base: a loop with
+                // Unrolled, with every operand a constant off the stage's base: a loop with
                 // run-time bounds moved each instruction's operands to uniform registers
-                // one by one and took 1000 cycles a step where the MMAs take 160 to 510.
-                // Inputs past K are zeros, so the last step runs whole as well.
+                // one by one and took 1000 cycles a tile of 256 inputs where the MMAs take 160
+                // to 510.  Inputs past K are zeros, so the last tile runs whole as well.
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    mx_copy_scales(sfa + 4 * g, st + MX_CODE_BYTES + 512 * g);
+                for (int h = 0; h < C::PER; ++h) {
+                    if (h == 1 && (m & MX_HALF)) break;
 #pragma unroll
-                    for (int c = 0; c < C::SF_CHUNKS; ++c)
-                        mx_copy_scales(sfb + 4 * (g * C::SF_CHUNKS + c), st + MX_TILE_BYTES + 512 * (g * C::SF_CHUNKS + c));
+                    for (int g = 0; g < 2; ++g) {
+                        mx_copy_scales(sfa + h * C::TILE_COLS + 4 * g, st + h * MX_TILE_BYTES + MX_CODE_BYTES + 512 * g);
+#pragma unroll
+                        for (int c = 0; c < C::SF_CHUNKS; ++c)
+                            mx_copy_scales(sfb + h * C::TILE_COLS + 4 * (g * C::SF_CHUNKS + c),
+                                           st + C::SFB_OFF + h * C::SFB_BYTES + 512 * (g * C::SF_CHUNKS + c));
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mx_mma(d, ad + h * (MX_TILE_BYTES >> 4) + 2 * kk, bd + h * (C::B_BYTES >> 4) + 2 * kk, kk & 1 ? idesc2 : idesc0,
+                               sfa + h * C::TILE_COLS + 4 * (kk >> 1), sfb + h * C::TILE_COLS + 4 * C::SF_CHUNKS * (kk >> 1),
+                               (h | kk) != 0 || !(m & MX_FIRST));
                 }
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mx_mma(d, ad + 2 * kk, bd + 2 * kk, kk & 1 ? idesc2 : idesc0, sfa + 4 * (kk >> 1),
-                           sfb + 4 * C::SF_CHUNKS * (kk >> 1), kk != 0 || !(m & MX_FIRST));
                 tc_commit(smem_u32(empty + s));
                 if (m & MX_LAST) tc_commit(smem_u32(acc_full + b));
             }
@@ -407,33 +425,32 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         mbar_drain(smem_u32(drain), 0, p.status);
     } else if (warp == 2 || warp == 12) {
         // ----------------------------------------------------------------- row scales
-        // Chunk (g, c) of a stage: 16 bytes for each l < 32, the four bytes of rows
-        // 128 c + 32 j + l, j < 4.  A lane takes the 16 bytes of a row for two steps at once;
-        // the two warps take such pairs of steps in turn and load one ahead, so a pair's loads
-        // have four steps to arrive.  (4-byte asynchronous copies, one for each word of a step,
-        // took 1140 cycles a step at 192 rows: 32 lines each.)
+        // Chunk (g, c) of an input tile: 16 bytes for each l < 32, the four bytes of rows
+        // 128 c + 32 j + l, j < 4.  A lane takes the 16 bytes of a row that two input tiles need;
+        // the two warps take such pairs of tiles in turn and load one ahead, so the loads have
+        // four tiles to arrive.  (4-byte asynchronous copies, one for each word, took 1140 cycles
+        // an input tile at 192 rows: 32 lines each.)
         constexpr int R = (C::NT + 31) / 32;
         const uint32_t which = warp == 2 ? 0 : 1;
         const int kb = p.K / MX_BLOCK, PT = (KT + 1) / 2;
         const bool aligned = kb % 16 == 0 && ((uintptr_t)p.a_scales & 15) == 0;
         uint32_t cur[R][4], nxt[R][4];
-        uint32_t it0 = 0;        // the tile's first step
-        uint32_t g = 0;          // pairs of steps before this one, all tiles
+        uint32_t it0 = 0;        // stages before this tile
+        uint32_t g = 0;          // pairs before the one in nxt, all tiles
         MxTile x{};
-        int pt = -1;             // the pair in nxt
-        uint32_t pt_it = 0;      // its first step
+        int pt = -1;             // the pair's place in the tile
         bool ok = true;
-        auto load = [&](int pair) {
+        auto load = [&]() {
 #pragma unroll
             for (int j = 0; j < R; ++j) {
                 if (32 * j >= x.n) break;
-                const uint8_t *src = p.a_scales + (size_t)(x.row0 + min(32 * j + lane, x.n - 1)) * kb + pair * 16;
+                const uint8_t *src = p.a_scales + (size_t)(x.row0 + min(32 * j + lane, x.n - 1)) * kb + pt * 16;
                 if (aligned) {
                     const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src));
                     nxt[j][0] = u.x; nxt[j][1] = u.y; nxt[j][2] = u.z; nxt[j][3] = u.w;
                 } else {
                     // aligned words that hold any of the row's bytes, shifted; bytes past K are 0
-                    const int left = kb - pair * 16;   // at least 1
+                    const int left = kb - pt * 16;   // at least 1
                     const uint32_t *word = reinterpret_cast<const uint32_t *>((uintptr_t)src & ~(uintptr_t)3);
                     const int off = (int)((uintptr_t)src & 3);
                     uint32_t v[5];
@@ -448,46 +465,41 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
                 }
             }
         };
-        // moves to this warp's next pair and loads it
+        // moves to this warp's next pair, at or behind pair g, and loads it
         auto advance = [&]() {
             while (walk.more()) {
                 if (pt < 0) x = walk.get();
                 for (++pt; pt < PT; ++pt, ++g)
-                    if ((g & 1) == which) {
-                        pt_it = it0 + 2 * pt;
-                        load(pt);
-                        ++g;
-                        return;
-                    }
+                    if ((g & 1) == which) return load();
                 pt = -1;
-                it0 += KT;
+                it0 += KS;
                 walk.next();
             }
         };
         advance();
         while (walk.more() && ok) {
-            const int chunk_rows = x.n, steps = min(2, KT - 2 * pt);
-            const uint32_t it = pt_it;
+            const int rows = x.n, first = 2 * pt;
+            const uint32_t it = it0 + first / C::PER;
 #pragma unroll
             for (int j = 0; j < R; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) cur[j][i] = nxt[j][i];
+            ++g;
             advance();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (h >= steps) break;
+            for (int h = 0; h < 2 / C::PER; ++h) {   // the pair's stages
+                if (first + h >= KT) break;
                 const uint32_t s = (it + h) % C::STAGES;
                 if (!(ok = mbar_wait(smem_u32(empty + s), (((it + h) / C::STAGES) & 1) ^ 1, abort, p.status))) break;
-                const uint32_t dst = smem_u32(stages + s * C::STAGE_BYTES) + MX_TILE_BYTES + lane * 16;
+                const uint32_t dst = smem_u32(stages + s * C::STAGE_BYTES) + C::SFB_OFF + lane * 16;
 #pragma unroll
                 for (int c = 0; c < C::SF_CHUNKS; ++c) {
-                    if (128 * c >= chunk_rows) break;
+                    if (128 * c >= rows) break;
+                    auto word = [&](int j, int i) { return 4 * c + j < R ? cur[4 * c + j < R ? 4 * c + j : 0][2 * h + i] : 0u; };
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        sts_v4(dst + 512 * (q * C::SF_CHUNKS + c),
-                               make_uint4(cur[4 * c][2 * h + q], 4 * c + 1 < R ? cur[4 * c + 1 < R ? 4 * c + 1 : 0][2 * h + q] : 0u,
-                                          4 * c + 2 < R ? cur[4 * c + 2 < R ? 4 * c + 2 : 0][2 * h + q] : 0u,
-                                          4 * c + 3 < R ? cur[4 * c + 3 < R ? 4 * c + 3 : 0][2 * h + q] : 0u));
+                    for (int i = 0; i < 2 * C::PER; ++i)   // input tile i / 2, 128 inputs i % 2 of it
+                        sts_v4(dst + (i >> 1) * C::SFB_BYTES + 512 * ((i & 1) * C::SF_CHUNKS + c),
+                               make_uint4(word(0, i), word(1, i), word(2, i), word(3, i)));
                 }
                 fence_proxy_async();
                 __syncwarp();

@@ -146,15 +146,17 @@ ds4moe_status run_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
     CK(h, cudaGetLastError());
     return DS4MOE_OK;
 }
-// Tiles of up to 32 rows with eight stages where experts have few rows, of up to 192 with five
-// elsewhere.  Measured (us, 32 rows / 192 rows a tile; 64 experts, 4096 x 4096, by the mean rows
-// an expert): 8 rows 108 / 106, 16 111 / 106, 32 110 / 109, 48 125 / 109, 96 197 / 113; and one row
-// each of 8 of 256 experts (gated, 2048 x 4096) 19.0 / 22.3, 40 rows of 32 experts 22.4 / 26.0:
-// with one or two rows the deeper ring wins, from 16 on the wider tile does.
+// Tiles of up to 32 rows, two steps a stage, where experts have few rows; of up to 192, one step a
+// stage, elsewhere.  Measured (us, 32 / 192 rows a tile; 64 experts, 4096 x 4096, by the mean rows
+// an expert): 8 rows 106 / 106, 16 109 / 106, 32 110 / 109, 48 125 / 109, 96 197 / 113; and one row
+// each of 8 of 256 experts (gated, 2048 x 4096) 17.6 / 22.3, 40 rows of 32 experts 21.9 / 26.0:
+// with one or two rows the deeper ring wins, from 16 on the wider tile does.  Two steps a stage
+// (half the barriers) took one row of one expert from 10.4 to 8.9 us; with wide tiles they leave
+// three stages of 128 rows or two of 192: 94 and 91 against 90 us at 8191 x 4096 x 4096.
 template <bool GATED>
 ds4moe_status pick_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
-    if (a.rows <= 12ll * std::min(a.rows, a.E)) return run_product<MxCfg<32, 16, 8, 8, GATED>>(h, a, st);
-    return run_product<MxCfg<192, 128, 64, 5, GATED>>(h, a, st);
+    if (a.rows <= 12ll * std::min(a.rows, a.E)) return run_product<MxCfg<32, 16, 8, 4, 2, GATED>>(h, a, st);
+    return run_product<MxCfg<192, 128, 64, 5, 1, GATED>>(h, a, st);
 }
 
 }  // namespace
