@@ -37,7 +37,9 @@ __device__ __forceinline__ void add_row(const T *p, float (&acc)[N]) {
 
 // y[t] = add[t] + sum_j w[t, j] o[inv_pos[t, j]]: the slots in order, in fp32, then add; a slot
 // whose row is outside [0, o_rows) adds nothing.  Bound by memory: every row of o is read once.
-// A thread takes 16 columns of a token; the rows of eight slots are in flight together.
+// A thread takes the columns of 32 bytes of a token; the rows of eight slots are in flight
+// together: 8192 x 7168 of 8, bf16 with an fp32 add, take 217 us (215 at a copy's rate; a column
+// a thread took 516).  Asking for add before the rows cost registers: 232 us.
 template <class TO, class TY>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ CombineArgs p, RowSplit split) {
     int t, first, last;

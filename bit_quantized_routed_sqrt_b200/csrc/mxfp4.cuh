@@ -37,7 +37,7 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
     const int e = (int)(amax_bits >> 23);   // a subnormal's 0 ends below 2 as well
     return e > 2 ? (uint32_t)(e - 2) : 0u;
 }
-// 2^-(s - 127) for a scale byte 0..252: exact, so x times it is x over the scale.
+// 2^-(s - 127) for a scale byte 0..252 (the largest of a finite block: 254 - 2): exact, so x times it is x over the scale.
 __device__ __forceinline__ float mx_inverse(uint32_t s) { return __uint_as_float((254u - s) << 23); }
 
 // ------------------------------------------------------------------ row types
@@ -114,7 +114,8 @@ struct RowSplit {
 // A thread takes 16 inputs (one or two 32-byte loads), two neighbours a block of 32.  Row r goes
 // to row r of the output, or to the rows inv_pos[r * k + j], j < k (entries outside [0, out_rows)
 // are skipped): the row is read and rounded once however many places it goes to.  Bound by
-// memory: bytes read once, written k times.
+// memory: 2048 x 4096 bf16 to 8 places each take 12.7 us cold (52 MB, 8 us at a copy's rate),
+// 8192 x 7168 70 us (56); with 8 inputs a thread and 16-byte loads 18 and 93.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(128) mxfp4_quantize_kernel(const T *__restrict__ x, int64_t ld, int K, RowSplit split,
                                                              const int *__restrict__ inv_pos, int k, int out_rows,
@@ -158,6 +159,8 @@ __global__ void __launch_bounds__(128) mxfp4_quantize_kernel(const T *__restrict
 
 // ------------------------------------------------------------------ dequantise
 // A thread takes 16 values: 8 bytes of codes and their scale byte to one or two 32-byte stores.
+// Bound by memory: 65536 x 7168 to bf16 take 183 us (181 at a copy's rate); with 8 values a
+// thread and 16-byte stores 259.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(128) mxfp4_dequantize_kernel(const uint8_t *__restrict__ codes,
                                                                const uint8_t *__restrict__ scales, int K, RowSplit split,

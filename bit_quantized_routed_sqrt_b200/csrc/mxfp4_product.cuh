@@ -311,18 +311,24 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    int decreasing = 0;   // groups would overlap and their tiles could outnumber what the host checked
     for (int e = threadIdx.x; e < p.E; e += MX_THREADS) {
         int first, last;
+        if (p.offsets && p.offsets[e] > p.offsets[e + 1]) decreasing = 1;
         mx_group(p, e, first, last);
         S[e] = (last - first + C::NT - 1) / C::NT;
         S[SR_MAX_EXPERTS + 1 + e] = first;
         S[2 * (SR_MAX_EXPERTS + 1) + e] = last;
     }
     tc_fence_before();
-    __syncthreads();
+    decreasing = __syncthreads_or(decreasing);
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    const int units = block_scan(S, p.E, part);
+    int units = block_scan(S, p.E, part);
+    if (decreasing) {   // no tile at all
+        units = 0;
+        if (threadIdx.x == 0) set_status(p.status, ST_EDEVICE);
+    }
     if (threadIdx.x == 0) S[p.E] = units;
     __syncthreads();
 

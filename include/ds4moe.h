@@ -334,7 +334,8 @@ void ds4moe_mxfp4_destroy(ds4moe_mxfp4 *h);
 /* Lay out the weights for the product, from device memory: codes_dev [E][N][K/2] (16-byte
  * aligned), scales_dev [E][N][K/32]; a gated handle takes the gate's and the up projection's
  * (both NULL otherwise).  Only enqueues; the sources may be freed once the stream has passed
- * it.  May be called again to replace the weights.  DS4MOE_FAULT=h2d applies. */
+ * it.  May be called again to replace the weights; products must be ordered
+ * behind it (the same stream, or an event).  DS4MOE_FAULT=h2d applies. */
 ds4moe_status ds4moe_mxfp4_load(ds4moe_mxfp4 *h, const uint8_t *codes_dev, const uint8_t *scales_dev,
                                 const uint8_t *up_codes_dev, const uint8_t *up_scales_dev, void *cuda_stream);
 
@@ -346,8 +347,9 @@ ds4moe_status ds4moe_mxfp4_load(ds4moe_mxfp4 *h, const uint8_t *codes_dev, const
  * (N % 32 == 0, ld == N) is quantised as by ds4moe_mxfp4_quantize into out_dev [rows][N/2]
  * (16-byte aligned) and out_scales_dev [rows][N/32] (NULL for the other types).  Rows behind
  * expert_offsets_dev[E] are neither used nor written.  Products whose magnitude is below the
- * normal range of fp32 may count as zero.  Offsets do not decrease; rows they claim beyond
- * `rows` do not count.  Calls of one handle may overlap on the device (it has no workspace),
+ * normal range of fp32 may count as zero.  Offsets must not decrease (if they do, nothing is
+ * written and ds4moe_mxfp4_sync_status reports DS4MOE_EDEVICE); rows they claim beyond `rows`
+ * do not count.  out must not overlap a.  Calls of one handle may overlap on the device (it has no workspace),
  * but not with ds4moe_mxfp4_load. */
 ds4moe_status ds4moe_mxfp4_product(ds4moe_mxfp4 *h, const uint8_t *a_codes_dev, const uint8_t *a_scales_dev, int32_t rows,
                                    const int32_t *expert_offsets_dev, void *out_dev, int32_t out_type, int64_t ld,
@@ -362,7 +364,7 @@ const char *ds4moe_mxfp4_last_error(const ds4moe_mxfp4 *h);
  * slots in order, in fp32, rounded once to y_type.  o_dev [o_rows][H], inv_pos_dev and
  * topk_w_dev [T][top_k]; a slot whose row is outside [0, o_rows) adds nothing, whatever its
  * weight.  add_dev [T][H] (the shared expert's rows) may be NULL, and may be y_dev itself
- * where the types are the same. */
+ * where the types are the same; y_dev overlaps no other input. */
 ds4moe_status ds4moe_combine(const void *o_dev, int32_t o_type, int64_t o_rows, int32_t T, int32_t top_k, int32_t H,
                              const int32_t *inv_pos_dev, const float *topk_w_dev, const void *add_dev, int32_t add_type,
                              void *y_dev, int32_t y_type, void *cuda_stream);

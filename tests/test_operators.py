@@ -463,6 +463,19 @@ def test_product_offsets_out_of_range_are_clipped(ds4):
     assert (np.abs(out.cpu().double().numpy() - want) <= bound + np.abs(want) * ref.U24).all()
 
 
+def test_product_refuses_offsets_that_decrease(ds4):
+    ex, mats = make(ds4, 3, 64, 256, False, 26)
+    codes, scales = (t.cuda() for t in mx_random((10, 256), gen(27)))
+    out = torch.full((10, 64), 9.0, device="cuda")
+    ex.product(codes, scales, torch.tensor([0, 8, 2, 10], dtype=torch.int32).cuda(), out)
+    with pytest.raises(ds4.Ds4MoeError, match="EDEVICE"):
+        ex.sync_status()
+    assert (out == 9.0).all()
+    ex.product(codes, scales, torch.tensor([0, 2, 8, 10], dtype=torch.int32).cuda(), out)
+    ex.sync_status()
+    assert (out != 9.0).all()
+
+
 def test_product_repeats_bit_for_bit(ds4):
     ex, mats = make(ds4, 4, 256, 4096, True, 28, centre=118)
     codes, scales = (t.cuda() for t in mx_random((9, 4096), gen(29)))
@@ -709,6 +722,30 @@ def test_calls_use_the_current_stream(ds4):
         got = c(*late)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_two_products_of_one_handle_at_once(ds4):
+    """A handle has no workspace: its calls may overlap on two streams."""
+    ex, mats = make(ds4, 4, 512, 1024, True, 60)
+    a = [tuple(t.cuda() for t in mx_random((40, 1024), gen(61 + i))) + (offsets_of(c).cuda(),)
+         for i, c in enumerate(([40, 0, 0, 0], [1, 13, 20, 6]))]
+    want = [ex.product(*x, torch.empty(40, 512, device="cuda")).clone() for x in a]
+    streams = [torch.cuda.Stream() for _ in a]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for x, s in zip(a, streams):
+            with torch.cuda.stream(s):
+                got.append(ex.product(*x, torch.zeros(40, 512, device="cuda")))
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    ex.sync_status()
+
+
+def test_routing_buffers_are_fixed(ds4):
+    b = ds4.Router(8, 2).buffers(3)
+    with pytest.raises(AttributeError):
+        b.topk_w = torch.empty(3, 2, device="cuda")
 
 
 def test_reload_replaces_the_weights(ds4):
