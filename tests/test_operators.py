@@ -153,9 +153,10 @@ def test_route_strided_rows_and_untouched_places(ds4):
     assert n < 200 and (out.sorted_token[n:] == -7).all() and (out.sorted_slot[n:] == -7).all()
 
 
-def test_route_many_tokens(ds4):
-    """The 256-token blocks of long calls: the last block ragged."""
-    logits = torch.randn(16385 + 77, 24, generator=gen(9))
+@pytest.mark.parametrize("T", [4700, 6000, 16462, 40000])
+def test_route_many_tokens(ds4, T):
+    """Few and many blocks, counts added up by every block or scanned, blocks of 32 to 128 tokens: the last ragged."""
+    logits = torch.randn(T, 24, generator=gen(9))
     check_route(ds4, logits, 3, torch.randn(24, generator=gen(1)) * 0.1, score="sigmoid")
 
 
