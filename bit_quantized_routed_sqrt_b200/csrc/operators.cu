@@ -229,15 +229,26 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
     ds4moe_status s = launched();
     if (s != DS4MOE_OK || !permute || a.NB == 1) return s;
     const int scanned = a.NB > SR_DIRECT;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.stream = st;
+    lc.attrs = at;
+    lc.numAttrs = 1;
     if (scanned) {
-        scored_scan_kernel<<<(a.E + 31) / 32, 1024, 0, st>>>(a);
-        if ((s = launched()) != DS4MOE_OK) return s;
+        lc.gridDim = dim3((a.E + 31) / 32);
+        lc.blockDim = dim3(1024);
+        if (cudaLaunchKernelEx(&lc, scored_scan_kernel, a) != cudaSuccess) return launched(), DS4MOE_ECUDA;
     }
     const size_t sums = scanned ? 0 : (size_t)2 * (SR_PERMUTE_THREADS / (a.pitch / 4)) * a.pitch;
     static_assert((2 * SR_MAX_EXPERTS + 2 * 4 * SR_PERMUTE_THREADS + SR_MAX_EXPERTS * (SR_MAX_BLOCK / 32)) * 4 <= 48 * 1024,
                   "shared memory of the permutation");
-    scored_permute_kernel<<<a.NB, SR_PERMUTE_THREADS, (2 * a.pitch + sums + (size_t)a.E * (a.TB / 32)) * 4, st>>>(a, scanned);
-    return launched();
+    lc.gridDim = dim3(a.NB);
+    lc.blockDim = dim3(SR_PERMUTE_THREADS);
+    lc.dynamicSmemBytes = (2 * a.pitch + sums + (size_t)a.E * (a.TB / 32)) * 4;
+    if (cudaLaunchKernelEx(&lc, scored_permute_kernel, a, scanned) != cudaSuccess) return launched(), DS4MOE_ECUDA;
+    return DS4MOE_OK;
 }
 
 ds4moe_status ds4moe_mxfp4_quantize(const void *x_dev, int32_t x_type, int64_t ld, int32_t rows, int32_t K,

@@ -5,7 +5,7 @@
 // l, which orders alike), the weight is that of s.  A warp per token; what bounds it is the
 // instructions of a token, not its bytes: 700 of them at 256 experts with a bias (300 the scores,
 // 160 the sort and the k picks, 120 the weights), 460 without, so 65536 tokens take 76 us for the
-// choice and 93 with the permutation where their 78 MB take 12 at a copy's rate.  Scores in fp64
+// choice and 89 with the permutation where their 78 MB take 12 at a copy's rate.  Scores in fp64
 // throughout took 520.  A single token takes 4.8 us of the GPU.
 #pragma once
 #include "combine.cuh"
@@ -497,6 +497,12 @@ __device__ __forceinline__ float scored_weight(const ScoredArgs &p, int64_t t, c
     return on ? w * p.scale : 0.0f;
 }
 
+// The kernels of one call are launched ahead of the end of the one before (programmatic
+// dependent launch): each lets the next start at once and waits, before it reads anything, for
+// the whole of the one before.  Measured: 65536 tokens 92.9 -> 89.4 us, 2048 tokens 9.9 -> 9.6.
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Positions of one block's pairs, given the first position of each expert's pairs of this
 // block (base) and the block's token masks.
 __device__ __forceinline__ void scored_scatter(const ScoredArgs &p, int t0, int nt, const int *base, const uint32_t *mask) {
@@ -522,6 +528,7 @@ __device__ __forceinline__ void scored_scatter(const ScoredArgs &p, int t0, int 
 // before the present one is chosen from.
 template <int NPL, class T, bool VEC, bool LONE>
 __global__ void __launch_bounds__(32 * (LONE ? SR_MAX_WARPS : SR_WARPS), LONE || NPL > 8 ? 1 : 3) scored_topk_kernel(const __grid_constant__ ScoredArgs p) {
+    next_kernel_may_start();
     extern __shared__ __align__(16) uint8_t sr_smem[];
     const int warps = blockDim.x >> 5, W = p.TB / 32;
     double *scratch = reinterpret_cast<double *>(sr_smem);                       // [warps][32 NPL], groups only
@@ -578,6 +585,8 @@ __global__ void __launch_bounds__(32 * (LONE ? SR_MAX_WARPS : SR_WARPS), LONE ||
 // Counts of the blocks -> the counts before each block, in place, and the totals.  A CTA has 32
 // experts, one a lane; its warps take runs of blocks.
 __global__ void __launch_bounds__(1024) scored_scan_kernel(const __grid_constant__ ScoredArgs p) {
+    next_kernel_may_start();
+    wait_for_kernel_before();
     __shared__ int sums[32][33];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
     const bool on = e < p.E;
@@ -613,6 +622,7 @@ __global__ void __launch_bounds__(1024) scored_scan_kernel(const __grid_constant
 // scored_scan_kernel; otherwise cnt holds the blocks' own counts, which every CTA adds up: four
 // experts a thread, the blocks dealt out to the strips of threads that the experts leave.
 __global__ void __launch_bounds__(SR_PERMUTE_THREADS) scored_permute_kernel(const __grid_constant__ ScoredArgs p, int scanned) {
+    wait_for_kernel_before();
     extern __shared__ __align__(16) uint8_t sr_smem[];
     const int W = p.TB / 32, fours = p.pitch / 4, strips = SR_PERMUTE_THREADS / fours;
     int *base = reinterpret_cast<int *>(sr_smem), *before = base + p.pitch;   // [pitch] each
