@@ -141,7 +141,6 @@ ds4moe_status run_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
     const int boxes[3] = {C::NT, C::BOX0, C::BOX1};
     for (int i = 0; i < 3; ++i)
         if (!row_map(&tm[i], a.a_codes, a.rows, a.K, boxes[i])) return fail(h, DS4MOE_ECUDA, "tensor map of the rows");
-    CK(h, cudaFuncSetAttribute(mxfp4_product_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM));
     mxfp4_product_kernel<C><<<h->num_sms, MX_THREADS, C::SMEM, st>>>(tm[0], tm[1], tm[2], a);
     CK(h, cudaGetLastError());
     return DS4MOE_OK;
@@ -154,9 +153,23 @@ ds4moe_status run_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
 // (half the barriers) took one row of one expert from 10.4 to 8.9 us; with wide tiles they leave
 // three stages of 128 rows or two of 192: 94 and 91 against 90 us at 8191 x 4096 x 4096.
 template <bool GATED>
+using FewRows = MxCfg<32, 16, 8, 4, 2, GATED>;
+template <bool GATED>
+using ManyRows = MxCfg<192, 128, 64, 5, 1, GATED>;
+template <bool GATED>
 ds4moe_status pick_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
-    if (a.rows <= 12ll * std::min(a.rows, a.E)) return run_product<MxCfg<32, 16, 8, 4, 2, GATED>>(h, a, st);
-    return run_product<MxCfg<192, 128, 64, 5, 1, GATED>>(h, a, st);
+    if (a.rows <= 12ll * std::min(a.rows, a.E)) return run_product<FewRows<GATED>>(h, a, st);
+    return run_product<ManyRows<GATED>>(h, a, st);
+}
+// The product kernels' shared memory on the current device (once, when a handle is made).
+template <class C>
+cudaError_t allow_smem() {
+    return cudaFuncSetAttribute(mxfp4_product_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+}
+template <bool GATED>
+cudaError_t prepare_product() {
+    const cudaError_t e = allow_smem<FewRows<GATED>>();
+    return e == cudaSuccess ? allow_smem<ManyRows<GATED>>() : e;
 }
 
 }  // namespace
@@ -357,6 +370,7 @@ ds4moe_status ds4moe_mxfp4_create(const ds4moe_mxfp4_config *cfg, int cuda_devic
     OnDevice on(cuda_device);
     cudaError_t e = on.err;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, cuda_device);
+    if (e == cudaSuccess) e = cfg->gated ? prepare_product<true>() : prepare_product<false>();
     if (e == cudaSuccess) e = cudaMalloc(&h->packed, h->expert_bytes * cfg->n_experts);
     if (e == cudaSuccess) e = cudaMalloc(&h->status, 256);
     if (e == cudaSuccess) e = cudaMemset(h->status, 0, 256);
