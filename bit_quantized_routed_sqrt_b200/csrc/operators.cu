@@ -147,18 +147,18 @@ ds4moe_status run_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
 }
 // Tiles of up to 32 rows, two steps a stage, where experts have few rows; of up to 192, one step a
 // stage, elsewhere.  Measured (us, 32 / 192 rows a tile; 64 experts, 4096 x 4096, by the mean rows
-// an expert): 8 rows 106 / 106, 16 109 / 106, 32 110 / 109, 48 125 / 109, 96 197 / 113; and one row
-// each of 8 of 256 experts (gated, 2048 x 4096) 17.6 / 22.3, 40 rows of 32 experts 21.9 / 26.0:
-// with one or two rows the deeper ring wins, from 16 on the wider tile does.  Two steps a stage
-// (half the barriers) took one row of one expert from 10.4 to 8.9 us; with wide tiles they leave
-// three stages of 128 rows or two of 192: 94 and 91 against 90 us at 8191 x 4096 x 4096.
+// an expert): 8 rows 106 / 106, 24 106 / 107, 32 106 / 108, 40 115 / 109; one row each of 8 of 256
+// experts (gated, 2048 x 4096) 17.6 / 22.3, 40 rows of 32 experts 21.9 / 26.0, one expert with 16
+// rows 9.2 / 10.4.  Two steps a stage (half the barriers) took one row of one expert from 10.4 to
+// 8.9 us; with wide tiles they leave three stages of 128 rows or two of 192: 94 and 91 against
+// 90 us at 8191 x 4096 x 4096.
 template <bool GATED>
 using FewRows = MxCfg<32, 16, 8, 4, 2, GATED>;
 template <bool GATED>
 using ManyRows = MxCfg<192, 128, 64, 5, 1, GATED>;
 template <bool GATED>
 ds4moe_status pick_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
-    if (a.rows <= 12ll * std::min(a.rows, a.E)) return run_product<FewRows<GATED>>(h, a, st);
+    if (a.rows <= 24ll * std::min(a.rows, a.E)) return run_product<FewRows<GATED>>(h, a, st);
     return run_product<ManyRows<GATED>>(h, a, st);
 }
 // The product kernels' shared memory on the current device (once, when a handle is made).
