@@ -42,12 +42,14 @@ __device__ __forceinline__ void add_row(const T *p, float (&acc)[N]) {
 // a thread took 516).  Asking for add before the rows cost registers: 232 us.
 template <class TO, class TY>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ CombineArgs p, RowSplit split) {
+    next_kernel_may_start();
+    wait_for_kernel_before();
     int t, first, last;
     split.place(t, first, last);
     const TO *o = reinterpret_cast<const TO *>(p.o);
     TY *y = reinterpret_cast<TY *>(p.y) + (size_t)t * p.H;
-    const int *inv = p.inv_pos + (size_t)t * p.k;
-    const float *w = p.w + (size_t)t * p.k;
+    const int *inv = after_wait(p.inv_pos) + (size_t)t * p.k;
+    const float *w = after_wait(p.w) + (size_t)t * p.k;
     constexpr int PER = 32 / sizeof(TO);   // a 32-byte load a row
     for (int g = first + threadIdx.x; g < last; g += blockDim.x) {
         float acc[PER];
@@ -100,11 +102,13 @@ template <class TO, class TY>
 __global__ void __launch_bounds__(128) combine_shifted_kernel(const __grid_constant__ CombineArgs p, RowSplit split) {
     constexpr int PER = 16 / sizeof(TO);
     __shared__ float buf[4][32 * (PER + 1)];
+    next_kernel_may_start();
+    wait_for_kernel_before();
     int t, first, last;
     split.place(t, first, last);
-    const uintptr_t base = (uintptr_t)p.o, end = base + (size_t)p.o_rows * p.H * sizeof(TO);
-    const int *inv = p.inv_pos + (size_t)t * p.k;
-    const float *w = p.w + (size_t)t * p.k;
+    const uintptr_t base = (uintptr_t)after_wait(p.o), end = base + (size_t)p.o_rows * p.H * sizeof(TO);
+    const int *inv = after_wait(p.inv_pos) + (size_t)t * p.k;
+    const float *w = after_wait(p.w) + (size_t)t * p.k;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int g0 = first + 32 * warp; g0 < last; g0 += 128) {   // 32 pieces a warp
         const int g = g0 + lane;

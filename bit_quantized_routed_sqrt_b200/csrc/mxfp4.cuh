@@ -98,6 +98,20 @@ __device__ __forceinline__ void store_row(T *p, const float (&v)[N]) {
     }
 }
 
+// Programmatic dependent launch: a kernel here lets the one behind it start at once, and waits
+// for the whole of the one before it, before it reads or writes any memory that both can see.
+// What overlaps is the launch and the set-up of barriers and tensor memory: one token's gated
+// product 17.5 -> 15.7 us, the routing of 2048 tokens (two kernels) 12.3 -> 10.0.
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A pointer whose read-only loads (which the compiler may move past other memory operations)
+// cannot move ahead of that wait.
+template <class T>
+__device__ __forceinline__ T *after_wait(T *p) {
+    asm volatile("" : "+l"(p)::"memory");
+    return p;
+}
+
 // Rows cut into segments of items, a CTA per segment (rows * segments CTAs): item i of a row on
 // thread i % blockDim.x.  Keeps a row's index arithmetic out of the items.
 struct RowSplit {
@@ -117,9 +131,13 @@ struct RowSplit {
 // memory: 2048 x 4096 bf16 to 8 places each take 12.7 us cold (52 MB, 8 us at a copy's rate),
 // 8192 x 7168 70 us (56); with 8 inputs a thread and 16-byte loads 18 and 93.
 template <class T, bool VEC>
-__global__ void __launch_bounds__(128) mxfp4_quantize_kernel(const T *__restrict__ x, int64_t ld, int K, RowSplit split,
-                                                             const int *__restrict__ inv_pos, int k, int out_rows,
-                                                             uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+__global__ void __launch_bounds__(128) mxfp4_quantize_kernel(const T *x, int64_t ld, int K, RowSplit split,
+                                                             const int *inv_pos, int k, int out_rows,
+                                                             uint8_t *codes, uint8_t *scales) {
+    next_kernel_may_start();
+    wait_for_kernel_before();
+    x = after_wait(x);
+    inv_pos = after_wait(inv_pos);
     int r, first, last;
     split.place(r, first, last);
     // items are K / 16 and segments even: the two threads of a block of 32 are in or out together
@@ -162,9 +180,13 @@ __global__ void __launch_bounds__(128) mxfp4_quantize_kernel(const T *__restrict
 // Bound by memory: 65536 x 7168 to bf16 take 183 us (181 at a copy's rate); with 8 values a
 // thread and 16-byte stores 259.
 template <class T, bool VEC>
-__global__ void __launch_bounds__(128) mxfp4_dequantize_kernel(const uint8_t *__restrict__ codes,
-                                                               const uint8_t *__restrict__ scales, int K, RowSplit split,
-                                                               T *__restrict__ out, int64_t ld) {
+__global__ void __launch_bounds__(128) mxfp4_dequantize_kernel(const uint8_t *codes,
+                                                               const uint8_t *scales, int K, RowSplit split,
+                                                               T *out, int64_t ld) {
+    next_kernel_may_start();
+    wait_for_kernel_before();
+    codes = after_wait(codes);
+    scales = after_wait(scales);
     int r, first, last;
     split.place(r, first, last);
 #pragma unroll 2
@@ -202,9 +224,15 @@ __host__ __device__ constexpr uint32_t mx_scale_off(int r, int blk) {
 }
 
 // One thread per (expert, packed row, block of 32 inputs), filler included.
-__global__ void __launch_bounds__(256) mxfp4_pack_kernel(const uint8_t *__restrict__ c0, const uint8_t *__restrict__ s0,
-                                                         const uint8_t *__restrict__ c1, const uint8_t *__restrict__ s1,
-                                                         int E, int N, int K, uint8_t *__restrict__ packed) {
+__global__ void __launch_bounds__(256) mxfp4_pack_kernel(const uint8_t *c0, const uint8_t *s0,
+                                                         const uint8_t *c1, const uint8_t *s1,
+                                                         int E, int N, int K, uint8_t *packed) {
+    next_kernel_may_start();
+    wait_for_kernel_before();
+    c0 = after_wait(c0);
+    s0 = after_wait(s0);
+    c1 = after_wait(c1);
+    s1 = after_wait(s1);
     const int mats = c1 ? 2 : 1, rows = N * mats;
     const int row_tiles = (rows + MX_TM - 1) / MX_TM, k_tiles = (K + MX_TK - 1) / MX_TK;
     const int64_t per_tile = MX_TM * (MX_TK / MX_BLOCK);

@@ -277,6 +277,7 @@ template <class C>
 __global__ void __launch_bounds__(MX_THREADS, 1)
     mxfp4_product_kernel(const __grid_constant__ CUtensorMap tm_nt, const __grid_constant__ CUtensorMap tm_box0,
                          const __grid_constant__ CUtensorMap tm_box1, const __grid_constant__ MxArgs p) {
+    next_kernel_may_start();
     extern __shared__ __align__(1024) uint8_t mx_smem_raw[];
     uint8_t *stages = mx_smem_raw + ((1024u - (smem_u32(mx_smem_raw) & 1023u)) & 1023u);
     uint8_t *epi = stages + C::STAGES * C::STAGE_BYTES;
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    wait_for_kernel_before();
     int decreasing = 0;   // groups would overlap and their tiles could outnumber what the host checked
     for (int e = threadIdx.x; e < p.E; e += MX_THREADS) {
         int first, last;
@@ -439,7 +441,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         constexpr int R = (C::NT + 31) / 32;
         const uint32_t which = warp == 2 ? 0 : 1;
         const int kb = p.K / MX_BLOCK, PT = (KT + 1) / 2;
-        const bool aligned = kb % 16 == 0 && ((uintptr_t)p.a_scales & 15) == 0;
+        const uint8_t *a_scales = after_wait(p.a_scales);
+        const bool aligned = kb % 16 == 0 && ((uintptr_t)a_scales & 15) == 0;
         uint32_t cur[R][4], nxt[R][4];
         uint32_t it0 = 0;        // stages before this tile
         uint32_t g = 0;          // pairs before the one in nxt, all tiles
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
 #pragma unroll
             for (int j = 0; j < R; ++j) {
                 if (32 * j >= x.n) break;
-                const uint8_t *src = p.a_scales + (size_t)(x.row0 + min(32 * j + lane, x.n - 1)) * kb + pt * 16;
+                const uint8_t *src = a_scales + (size_t)(x.row0 + min(32 * j + lane, x.n - 1)) * kb + pt * 16;
                 if (aligned) {
                     const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src));
                     nxt[j][0] = u.x; nxt[j][1] = u.y; nxt[j][2] = u.z; nxt[j][3] = u.w;

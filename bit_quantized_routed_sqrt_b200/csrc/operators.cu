@@ -42,7 +42,6 @@ bool injected(const char *what) {
 }
 bool float_type(int t) { return t == DS4MOE_F32 || t == DS4MOE_BF16 || t == DS4MOE_F16; }
 size_t size_of(int t) { return t == DS4MOE_F32 ? 4 : 2; }
-ds4moe_status launched() { return cudaGetLastError() == cudaSuccess ? DS4MOE_OK : DS4MOE_ECUDA; }
 
 ds4moe_status fail(ds4moe_mxfp4 *h, ds4moe_status st, const char *fmt, ...) {
     char buf[512];
@@ -86,6 +85,26 @@ RowSplit split_rows(int64_t rows, int items, int most) {
     if (rows * s.segments > INT32_MAX) s.segments = 1;
     s.per = ((items + s.segments - 1) / s.segments + 1) & ~1;
     return s;
+}
+// A launch that may begin before the kernel ahead of it in the stream has ended; every kernel
+// here waits for that end itself.
+template <class... P, class... A>
+cudaError_t launch_ahead(void (*kernel)(P...), int grid, int block, size_t smem, cudaStream_t st, A &&...args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(block);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, static_cast<P>(args)...);
+}
+ds4moe_status launched(cudaError_t e) {
+    if (e != cudaSuccess) cudaGetLastError();   // the next call's launch does not report it
+    return e == cudaSuccess ? DS4MOE_OK : DS4MOE_ECUDA;
 }
 int blocks_for(int64_t threads) { return (int)std::min<int64_t>((threads + 255) / 256, 148 * 64); }
 
@@ -141,16 +160,15 @@ ds4moe_status run_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
     const int boxes[3] = {C::NT, C::BOX0, C::BOX1};
     for (int i = 0; i < 3; ++i)
         if (!row_map(&tm[i], a.a_codes, a.rows, a.K, boxes[i])) return fail(h, DS4MOE_ECUDA, "tensor map of the rows");
-    mxfp4_product_kernel<C><<<h->num_sms, MX_THREADS, C::SMEM, st>>>(tm[0], tm[1], tm[2], a);
-    CK(h, cudaGetLastError());
+    CK(h, launch_ahead(mxfp4_product_kernel<C>, h->num_sms, MX_THREADS, C::SMEM, st, tm[0], tm[1], tm[2], a));
     return DS4MOE_OK;
 }
 // Tiles of up to 32 rows, two steps a stage, where experts have few rows; of up to 192, one step a
 // stage, elsewhere.  Measured (us, 32 / 192 rows a tile; 64 experts, 4096 x 4096, by the mean rows
 // an expert): 8 rows 106 / 106, 24 106 / 107, 32 106 / 108, 40 115 / 109; one row each of 8 of 256
 // experts (gated, 2048 x 4096) 17.6 / 22.3, 40 rows of 32 experts 21.9 / 26.0, one expert with 16
-// rows 9.2 / 10.4.  Two steps a stage (half the barriers) took one row of one expert from 10.4 to
-// 8.9 us; with wide tiles they leave three stages of 128 rows or two of 192: 94 and 91 against
+// rows 9.2 / 10.4 (all before kernels were launched ahead).  Two steps a stage (half the barriers)
+// took one row of one expert from 10.4 to 8.9 us; with wide tiles they leave three stages of 128 rows or two of 192: 94 and 91 against
 // 90 us at 8191 x 4096 x 4096.
 template <bool GATED>
 using FewRows = MxCfg<32, 16, 8, 4, 2, GATED>;
@@ -215,11 +233,12 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
     // one block, or fewer than the SMs: more warps a block, two tokens a warp
     const bool few = a.NB <= 148;
     const int warps = few ? std::min(std::max(std::min(T, a.TB) / 2, SR_WARPS), SR_MAX_WARPS) : SR_WARPS;
+    cudaError_t err = cudaSuccess;
     auto launch = [&](auto many, auto lone, int npl) {
         auto kernel = few ? lone : many;
         const size_t smem = (a.G > 1 ? (size_t)warps * 32 * npl * 8 : 0) + (size_t)a.E * (a.TB / 32 + 1) * 4;
-        if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        kernel<<<a.NB, 32 * warps, smem, st>>>(a);
+        if (smem > 48 * 1024) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (err == cudaSuccess) err = launch_ahead(kernel, a.NB, 32 * warps, smem, st, a);
     };
     static_assert(SR_MAX_WARPS * SR_MAX_EXPERTS * 8 + SR_MAX_EXPERTS * (SR_MAX_BLOCK / 32 + 1) * 4 <= 227 * 1024,
                   "shared memory per CTA");
@@ -239,29 +258,14 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
     if (logits_type == DS4MOE_F32) typed(float{});
     else if (logits_type == DS4MOE_BF16) typed(__nv_bfloat16{});
     else typed(__half{});
-    ds4moe_status s = launched();
-    if (s != DS4MOE_OK || !permute || a.NB == 1) return s;
+    if (err != cudaSuccess || !permute || a.NB == 1) return launched(err);
     const int scanned = a.NB > SR_DIRECT;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t lc = {};
-    lc.stream = st;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    if (scanned) {
-        lc.gridDim = dim3((a.E + 31) / 32);
-        lc.blockDim = dim3(1024);
-        if (cudaLaunchKernelEx(&lc, scored_scan_kernel, a) != cudaSuccess) return launched(), DS4MOE_ECUDA;
-    }
+    if (scanned && (err = launch_ahead(scored_scan_kernel, (a.E + 31) / 32, 1024, 0, st, a)) != cudaSuccess) return launched(err);
     const size_t sums = scanned ? 0 : (size_t)2 * (SR_PERMUTE_THREADS / (a.pitch / 4)) * a.pitch;
     static_assert((2 * SR_MAX_EXPERTS + 2 * 4 * SR_PERMUTE_THREADS + SR_MAX_EXPERTS * (SR_MAX_BLOCK / 32)) * 4 <= 48 * 1024,
                   "shared memory of the permutation");
-    lc.gridDim = dim3(a.NB);
-    lc.blockDim = dim3(SR_PERMUTE_THREADS);
-    lc.dynamicSmemBytes = (2 * a.pitch + sums + (size_t)a.E * (a.TB / 32)) * 4;
-    if (cudaLaunchKernelEx(&lc, scored_permute_kernel, a, scanned) != cudaSuccess) return launched(), DS4MOE_ECUDA;
-    return DS4MOE_OK;
+    return launched(launch_ahead(scored_permute_kernel, a.NB, SR_PERMUTE_THREADS,
+                                 (2 * a.pitch + sums + (size_t)a.E * (a.TB / 32)) * 4, st, a, scanned));
 }
 
 ds4moe_status ds4moe_mxfp4_quantize(const void *x_dev, int32_t x_type, int64_t ld, int32_t rows, int32_t K,
@@ -275,8 +279,10 @@ ds4moe_status ds4moe_mxfp4_quantize(const void *x_dev, int32_t x_type, int64_t l
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
     const bool vec = aligned32(x_dev) && ld * size_of(x_type) % 32 == 0;
     const RowSplit split = split_rows(rows, K / 16, 4);
+    cudaError_t err = cudaSuccess;
     auto go = [&](auto kernel, auto *x) {
-        kernel<<<rows * split.segments, 128, 0, st>>>(x, ld, K, split, inv_pos_dev, top_k, out_rows, codes_dev, scales_dev);
+        err = launch_ahead(kernel, rows * split.segments, 128, 0, st, x, ld, K, split, inv_pos_dev, top_k, out_rows, codes_dev,
+                           scales_dev);
     };
     if (x_type == DS4MOE_F32) {
         auto *x = static_cast<const float *>(x_dev);
@@ -288,7 +294,7 @@ ds4moe_status ds4moe_mxfp4_quantize(const void *x_dev, int32_t x_type, int64_t l
         auto *x = static_cast<const __half *>(x_dev);
         if (vec) go(mxfp4_quantize_kernel<__half, true>, x); else go(mxfp4_quantize_kernel<__half, false>, x);
     }
-    return launched();
+    return launched(err);
 }
 
 ds4moe_status ds4moe_mxfp4_dequantize(const uint8_t *codes_dev, const uint8_t *scales_dev, int32_t rows, int32_t K,
@@ -300,8 +306,9 @@ ds4moe_status ds4moe_mxfp4_dequantize(const uint8_t *codes_dev, const uint8_t *s
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
     const bool vec = aligned32(out_dev) && ld * size_of(out_type) % 32 == 0;
     const RowSplit split = split_rows(rows, K / 16, 4);
+    cudaError_t err = cudaSuccess;
     auto go = [&](auto kernel, auto *out) {
-        kernel<<<rows * split.segments, 128, 0, st>>>(codes_dev, scales_dev, K, split, out, ld);
+        err = launch_ahead(kernel, rows * split.segments, 128, 0, st, codes_dev, scales_dev, K, split, out, ld);
     };
     if (out_type == DS4MOE_F32) {
         auto *o = static_cast<float *>(out_dev);
@@ -313,7 +320,7 @@ ds4moe_status ds4moe_mxfp4_dequantize(const uint8_t *codes_dev, const uint8_t *s
         auto *o = static_cast<__half *>(out_dev);
         if (vec) go(mxfp4_dequantize_kernel<__half, true>, o); else go(mxfp4_dequantize_kernel<__half, false>, o);
     }
-    return launched();
+    return launched(err);
 }
 
 ds4moe_status ds4moe_combine(const void *o_dev, int32_t o_type, int64_t o_rows, int32_t T, int32_t top_k, int32_t H,
@@ -335,7 +342,8 @@ ds4moe_status ds4moe_combine(const void *o_dev, int32_t o_type, int64_t o_rows, 
                      H * size_of(y_type) % 16 == 0 && (!add_dev || aligned16(add_dev));
     const int piece = 16 / size_of(o_type);
     const RowSplit split = split_rows(T, vec ? H / per : (H + piece - 1) / piece, 4);
-    auto go = [&](auto kernel) { kernel<<<T * split.segments, 128, 0, st>>>(a, split); };
+    cudaError_t err = cudaSuccess;
+    auto go = [&](auto kernel) { err = launch_ahead(kernel, T * split.segments, 128, 0, st, a, split); };
     auto with = [&](auto o) {
         using TO = decltype(o);
         auto to = [&](auto y) {
@@ -350,7 +358,7 @@ ds4moe_status ds4moe_combine(const void *o_dev, int32_t o_type, int64_t o_rows, 
     if (o_type == DS4MOE_F32) with(float{});
     else if (o_type == DS4MOE_BF16) with(__nv_bfloat16{});
     else with(__half{});
-    return launched();
+    return launched(err);
 }
 
 const char *ds4moe_mxfp4_last_error(const ds4moe_mxfp4 *h) { return h ? h->err.c_str() : "null handle"; }
@@ -408,9 +416,8 @@ ds4moe_status ds4moe_mxfp4_load(ds4moe_mxfp4 *h, const uint8_t *codes_dev, const
     CK(h, on.err);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
     const int64_t n = (int64_t)g.n_experts * (h->expert_bytes / MX_TILE_BYTES) * MX_TM * (MX_TK / MX_BLOCK);
-    mxfp4_pack_kernel<<<blocks_for(n), 256, 0, st>>>(codes_dev, scales_dev, g.gated ? up_codes_dev : nullptr,
-                                                    g.gated ? up_scales_dev : nullptr, g.n_experts, g.n_out, g.n_in, h->packed);
-    CK(h, cudaGetLastError());
+    CK(h, launch_ahead(mxfp4_pack_kernel, blocks_for(n), 256, 0, st, codes_dev, scales_dev, g.gated ? up_codes_dev : nullptr,
+                       g.gated ? up_scales_dev : nullptr, g.n_experts, g.n_out, g.n_in, h->packed));
     h->loaded = true;
     h->last_stream = st;
     return DS4MOE_OK;

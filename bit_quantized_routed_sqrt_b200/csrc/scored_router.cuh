@@ -5,8 +5,8 @@
 // l, which orders alike), the weight is that of s.  A warp per token; what bounds it is the
 // instructions of a token, not its bytes: 700 of them at 256 experts with a bias (300 the scores,
 // 160 the sort and the k picks, 120 the weights), 460 without, so 65536 tokens take 76 us for the
-// choice and 89 with the permutation where their 78 MB take 12 at a copy's rate.  Scores in fp64
-// throughout took 520.  A single token takes 4.8 us of the GPU.
+// choice and 88 with the permutation where their 78 MB take 12 at a copy's rate.  Scores in fp64
+// throughout took 520.  A single token takes 4.4 us of the GPU.
 #pragma once
 #include "combine.cuh"
 #include "scan.cuh"
@@ -234,9 +234,9 @@ struct LaneLogits {
     T v[VEC ? 1 : NPL];
 
     __device__ __forceinline__ static int expert(int lane, int i) { return VEC ? lane * NPL + i : lane + 32 * i; }
-    __device__ __forceinline__ void load(const ScoredArgs &p, int64_t t) {
+    __device__ __forceinline__ void load(const ScoredArgs &p, const T *logits, int64_t t) {
         const int lane = threadIdx.x & 31;
-        const T *row = reinterpret_cast<const T *>(p.logits) + t * p.ld;
+        const T *row = logits + t * p.ld;
         if constexpr (VEC) {
             const uint8_t *src = reinterpret_cast<const uint8_t *>(row) + lane * BYTES;
             if constexpr (BYTES % 16 == 0) {
@@ -497,12 +497,6 @@ __device__ __forceinline__ float scored_weight(const ScoredArgs &p, int64_t t, c
     return on ? w * p.scale : 0.0f;
 }
 
-// The kernels of one call are launched ahead of the end of the one before (programmatic
-// dependent launch): each lets the next start at once and waits, before it reads anything, for
-// the whole of the one before.  Measured: 65536 tokens 92.9 -> 89.4 us, 2048 tokens 9.9 -> 9.6.
-__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Positions of one block's pairs, given the first position of each expert's pairs of this
 // block (base) and the block's token masks.
 __device__ __forceinline__ void scored_scatter(const ScoredArgs &p, int t0, int nt, const int *base, const uint32_t *mask) {
@@ -529,6 +523,7 @@ __device__ __forceinline__ void scored_scatter(const ScoredArgs &p, int t0, int 
 template <int NPL, class T, bool VEC, bool LONE>
 __global__ void __launch_bounds__(32 * (LONE ? SR_MAX_WARPS : SR_WARPS), LONE || NPL > 8 ? 1 : 3) scored_topk_kernel(const __grid_constant__ ScoredArgs p) {
     next_kernel_may_start();
+    wait_for_kernel_before();
     extern __shared__ __align__(16) uint8_t sr_smem[];
     const int warps = blockDim.x >> 5, W = p.TB / 32;
     double *scratch = reinterpret_cast<double *>(sr_smem);                       // [warps][32 NPL], groups only
@@ -538,7 +533,8 @@ __global__ void __launch_bounds__(32 * (LONE ? SR_MAX_WARPS : SR_WARPS), LONE ||
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * p.TB, nt = min(p.TB, p.T - t0);
     LaneLogits<NPL, T, VEC> now, next;
-    if (warp < nt) next.load(p, t0 + warp);
+    const T *logits = after_wait(reinterpret_cast<const T *>(p.logits));
+    if (warp < nt) next.load(p, logits, t0 + warp);
     float bias[NPL], bias_size = 0.0f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
@@ -551,7 +547,7 @@ __global__ void __launch_bounds__(32 * (LONE ? SR_MAX_WARPS : SR_WARPS), LONE ||
     __syncthreads();
     for (int tl = warp; tl < nt; tl += warps) {
         now = next;
-        if (tl + warps < nt) next.load(p, t0 + tl + warps);
+        if (tl + warps < nt) next.load(p, logits, t0 + tl + warps);
         const int e = scored_choice<NPL, T, VEC>(p, t0 + tl, now, bias, bias_size, scratch + (p.G > 1 ? warp * 32 * NPL : 0));
         const float w = scored_weight<NPL, T, VEC>(p, t0 + tl, now, e);
         if (lane < p.k) {
@@ -622,6 +618,7 @@ __global__ void __launch_bounds__(1024) scored_scan_kernel(const __grid_constant
 // scored_scan_kernel; otherwise cnt holds the blocks' own counts, which every CTA adds up: four
 // experts a thread, the blocks dealt out to the strips of threads that the experts leave.
 __global__ void __launch_bounds__(SR_PERMUTE_THREADS) scored_permute_kernel(const __grid_constant__ ScoredArgs p, int scanned) {
+    next_kernel_may_start();
     wait_for_kernel_before();
     extern __shared__ __align__(16) uint8_t sr_smem[];
     const int W = p.TB / 32, fours = p.pitch / 4, strips = SR_PERMUTE_THREADS / fours;

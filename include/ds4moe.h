@@ -242,7 +242,8 @@ ds4moe_status ds4moe_get_trace(ds4moe *h, int64_t *out, int32_t max_records, int
  * Calls without a handle launch on the calling thread's current device, which must be that
  * of the buffers and the stream; they keep nothing and may run concurrently on different
  * outputs and workspaces.  They return DS4MOE_EINVAL for an argument out of range, NULL or
- * misaligned.  Every call here only enqueues work (none allocates), so it can be captured
+ * misaligned.  Apart from making, freeing and asking the status of a handle, a call only
+ * enqueues work and allocates nothing, so it can be captured
  * into a CUDA graph.  The library has no training path: none of these has a backward pass.
  * Element types: */
 typedef enum {
