@@ -172,6 +172,8 @@ __device__ __noinline__ int scored_choice64(const ScoredArgs &p, int64_t t, doub
 
 constexpr uint32_t SR_LIVE = 0x00800000u;   // the lowest key of a finite value
 
+// Bits that order as the values do, -0 below +0: where the two are a tie (logits; a score is not -0,
+// nor its sum with a bias) 0 is added to the value first.
 __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t u = __float_as_uint(v);
     return (u >> 31) ? ~u : (u | 0x80000000u);
@@ -358,6 +360,9 @@ __device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, con
             for (int i = 0; i < NPL; ++i) take(i, score(a[i]));
         }
         M = fmaf(off, 2.384185791e-7f, fmaf(most + bias_size, 1.192092896e-7f, 2e-19f));
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) a[i] += 0.0f;   // -0 and +0 are equal logits
     }
     uint32_t key[NPL];
 #pragma unroll
@@ -402,7 +407,7 @@ __device__ __forceinline__ int scored_choice(const ScoredArgs &p, int64_t t, con
             const int of = (int)(((float)L::expert(lane, i) + 0.5f) * inv);
             if (!((kept >> (of & 31)) & 1u)) key[i] = 0u;
             else if (!p.bias && by_score && key[i] >= SR_LIVE)   // ranked by the logit, chosen groups by their scores
-                key[i] = (order_key(logits.get(p, i)) & ~LOW) | (LOW - (uint32_t)L::expert(lane, i));
+                key[i] = (order_key(logits.get(p, i) + 0.0f) & ~LOW) | (LOW - (uint32_t)L::expert(lane, i));
         }
         if (!p.bias) M = 0.0f;
     }

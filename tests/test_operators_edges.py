@@ -1,0 +1,38 @@
+"""The operators beside the layer at their edges: values, sizes and calls that the other tests leave out."""
+import pytest
+
+torch = pytest.importorskip("torch")
+from test_operators import TYPES, check_route, ds4, gen  # noqa: E402, F401  (ds4: the fixture)
+
+
+# ------------------------------------------------------------------ signed zeros
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("E", [3, 64, 128, 200, 256, 512])
+def test_zeros_of_both_signs_are_a_tie(ds4, kind, E):
+    """-0 and +0 are equal logits: the lower index goes first, in the order and at the k-th place."""
+    g = gen(E)
+    some = torch.tensor([-1.0, -0.0, 0.0, -0.0, 0.0, 1.0])
+    logits = some[torch.randint(0, 6, (90, E), generator=g)]
+    logits[0], logits[1] = -0.0, 0.0
+    logits[2, 0::2], logits[2, 1::2] = -0.0, 0.0
+    logits[3, 0::2], logits[3, 1::2] = 0.0, -0.0
+    logits[4], logits[4, E - 1], logits[4, E - 2] = -1.0, 0.0, -0.0       # the last places, in turn
+    logits[5], logits[5, E - 1], logits[5, 0], logits[5, 1] = -0.0, 5.0, -0.0, 0.0
+    logits = logits.to(TYPES[kind])
+    assert bool(torch.signbit(logits[0, 0])) and not bool(torch.signbit(logits[1, 0]))
+    for bias in (None, torch.zeros(E), -torch.zeros(E)):
+        for score in ("softmax", "sigmoid", "sqrt_softplus"):
+            check_route(ds4, logits, 1, bias, score=score)
+            check_route(ds4, logits, min(E, 8), bias, score=score, renormalise=False)
+            if E % 4 == 0:
+                for group_score in ("max", "top2"):
+                    check_route(ds4, logits, 8, bias, score=score, n_groups=4, topk_groups=2, group_score=group_score)
+
+
+@pytest.mark.gpu
+def test_zeros_by_underflow_are_a_tie(ds4):
+    """Products that underflow to -0 and +0 in fp16, with a +0 of a higher index."""
+    logits = torch.tensor([[-1e-9, 1e-9, -1.0], [1e-9, -1e-9, -1.0], [-1.0, -1e-9, 1e-9]]).half()
+    check_route(ds4, logits, 1)
+    check_route(ds4, logits, 2)
