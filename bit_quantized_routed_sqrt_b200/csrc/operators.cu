@@ -237,7 +237,7 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
     auto launch = [&](auto many, auto lone, int npl) {
         auto kernel = few ? lone : many;
         const size_t smem = (a.G > 1 ? (size_t)warps * 32 * npl * 8 : 0) + (size_t)a.E * (a.TB / 32 + 1) * 4;
-        if (smem > 48 * 1024) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (smem > SR_PLAIN_SMEM) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (err == cudaSuccess) err = launch_ahead(kernel, a.NB, 32 * warps, smem, st, a);
     };
     static_assert(SR_MAX_WARPS * SR_MAX_EXPERTS * 8 + SR_MAX_EXPERTS * (SR_MAX_BLOCK / 32 + 1) * 4 <= 227 * 1024,

@@ -19,6 +19,9 @@ constexpr int SR_MIN_BLOCK = 32, SR_MAX_BLOCK = 256;     // tokens a CTA
 constexpr int SR_WARPS = 8, SR_MAX_WARPS = 16;           // warps a CTA (a lone CTA: up to 16)
 constexpr int SR_DIRECT = 256;                           // blocks whose counts every CTA adds up itself
 constexpr int SR_PERMUTE_THREADS = 512;
+// Dynamic shared memory that a launch may have without leave: 48 KB less what the kernel has
+// beside it, 32 bytes that the compiler makes 1 KB of (with room for more of both).
+constexpr int SR_PLAIN_SMEM = 44 * 1024;
 
 enum : int { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1, SCORE_SQRT_SOFTPLUS = 2 };
 

@@ -1,8 +1,17 @@
 """The operators beside the layer at their edges: values, sizes and calls that the other tests leave out."""
+import os
+import subprocess
+import sys
+
+import numpy as np
 import pytest
+
+import operator_refs as ref
 
 torch = pytest.importorskip("torch")
 from test_operators import TYPES, check_route, ds4, gen  # noqa: E402, F401  (ds4: the fixture)
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 # ------------------------------------------------------------------ signed zeros
@@ -36,3 +45,30 @@ def test_zeros_by_underflow_are_a_tie(ds4):
     logits = torch.tensor([[-1e-9, 1e-9, -1.0], [1e-9, -1e-9, -1.0], [-1.0, -1e-9, 1e-9]]).half()
     check_route(ds4, logits, 1)
     check_route(ds4, logits, 2)
+
+
+# ------------------------------------------------------------------ shared memory of the routing
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,G,T", [(336, 4, 22), (340, 4, 22), (339, 3, 23), (341, 11, 22), (455, 5, 76001)])
+def test_route_at_the_limit_of_plain_shared_memory(ds4, E, G, T):
+    """Dynamic sizes within the kernel's own static bytes of 48 KB, each in a process of its own (an earlier call
+    could have raised the kernel's limit)."""
+    program = """
+import torch, numpy as np
+import bit_quantized_routed_sqrt_b200 as ds4
+import operator_refs as ref
+E, G, T = %d, %d, %d
+logits = torch.randn(T, E, generator=torch.Generator().manual_seed(E))
+r = ds4.Router(E, 4, n_groups=G, topk_groups=2).route(logits.cuda())
+torch.cuda.synchronize()
+rows = list(range(min(T, 40))) + ([T - 1] if T > 40 else [])
+idx, w = ref.route(logits[rows], 4, "softmax", None, G, 2)
+got = r.topk_idx.cpu().numpy()
+assert np.array_equal(got[rows], idx)
+off, st, ss, inv = ref.permute(got, E)
+assert np.array_equal(r.expert_offsets.cpu().numpy(), off) and np.array_equal(r.inv_pos.cpu().numpy(), inv)
+assert np.array_equal(r.sorted_token.cpu().numpy(), st) and np.array_equal(r.sorted_slot.cpu().numpy(), ss)
+""" % (E, G, T)
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([ROOT, os.path.join(ROOT, "tests")]))
+    done = subprocess.run([sys.executable, "-c", program], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
