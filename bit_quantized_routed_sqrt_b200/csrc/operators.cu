@@ -237,11 +237,13 @@ ds4moe_status ds4moe_route_logits(const ds4moe_router *r, const void *logits_dev
     auto launch = [&](auto many, auto lone, int npl) {
         auto kernel = few ? lone : many;
         const size_t smem = (a.G > 1 ? (size_t)warps * 32 * npl * 8 : 0) + (size_t)a.E * (a.TB / 32 + 1) * 4;
-        if (smem > SR_PLAIN_SMEM) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // The leave is the kernel's, for every thread of the process, so it is always for the most
+        // that any call takes: it never falls below what another thread is about to launch with.
+        if (smem > SR_PLAIN_SMEM)
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SR_MOST_SMEM);
         if (err == cudaSuccess) err = launch_ahead(kernel, a.NB, 32 * warps, smem, st, a);
     };
-    static_assert(SR_MAX_WARPS * SR_MAX_EXPERTS * 8 + SR_MAX_EXPERTS * (SR_MAX_BLOCK / 32 + 1) * 4 <= 227 * 1024,
-                  "shared memory per CTA");
+    static_assert(SR_MOST_SMEM + 4096 <= 227 * 1024, "shared memory per CTA");
     auto typed = [&](auto v) {
         using E = decltype(v);
         // a lane's logits as one aligned piece: the common counts of experts

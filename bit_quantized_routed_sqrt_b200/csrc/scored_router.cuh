@@ -22,6 +22,8 @@ constexpr int SR_PERMUTE_THREADS = 512;
 // Dynamic shared memory that a launch may have without leave: 48 KB less what the kernel has
 // beside it, 32 bytes that the compiler makes 1 KB of (with room for more of both).
 constexpr int SR_PLAIN_SMEM = 44 * 1024;
+// the most dynamic shared memory of one: values of every warp's experts (groups), masks and counts
+constexpr int SR_MOST_SMEM = SR_MAX_WARPS * SR_MAX_EXPERTS * 8 + SR_MAX_EXPERTS * (SR_MAX_BLOCK / 32 + 1) * 4;
 
 enum : int { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1, SCORE_SQRT_SOFTPLUS = 2 };
 

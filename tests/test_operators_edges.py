@@ -2,6 +2,7 @@
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -72,3 +73,35 @@ assert np.array_equal(r.sorted_token.cpu().numpy(), st) and np.array_equal(r.sor
     env = dict(os.environ, PYTHONPATH=os.pathsep.join([ROOT, os.path.join(ROOT, "tests")]))
     done = subprocess.run([sys.executable, "-c", program], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+@pytest.mark.gpu
+def test_route_from_several_threads(ds4):
+    """Calls of host threads at once that need different amounts of shared memory of the same kernel."""
+    state, want = [], []
+    for E, T in [(508, 64), (300, 24), (508, 64), (300, 24)]:
+        r = ds4.Router(E, 4, n_groups=4, topk_groups=2)
+        logits = torch.randn(T, E, generator=gen(E)).cuda()
+        out, stream = r.buffers(T), torch.cuda.Stream()
+        args = [ds4.C.byref(r.cfg), logits.data_ptr(), ds4.F32, E, T, None, *out.addresses, stream.cuda_stream]
+        state.append((args, out, r, logits, stream))
+        want.append(r.route(logits).topk_idx.clone())
+    torch.cuda.synchronize()
+    wrong = [0] * len(state)
+    start = threading.Barrier(len(state))
+
+    def work(i):   # the library's call alone, so that the threads meet inside it
+        args, call = state[i][0], ds4.lib.ds4moe_route_logits
+        start.wait(30)
+        for _ in range(30000):
+            wrong[i] += call(*args) != 0
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(state))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert wrong == [0] * len(state)
+    for s, w in zip(state, want):
+        assert torch.equal(s[1].topk_idx, w)
