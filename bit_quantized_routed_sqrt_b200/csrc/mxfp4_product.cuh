@@ -175,7 +175,28 @@ struct MxTiles {
     }
 };
 
-__device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + expf(-g)); }
+// silu(g) u = g u / (1 + e^-g).  Below SILU_FAR e^-g leaves the range where __fdividef divides (its
+// result is 0 for divisors above 2^126), though the product may be a normal value; there 1 + e^-g is
+// e^-g to the last bit, and each half of e^g goes to one factor.  The operands of one quotient are
+// selected: selecting the quotient itself makes a branch of it (16384 rows, 2 x 2048 x 4096: 454 us
+// against 480).
+constexpr float SILU_FAR = -87.0f;
+__device__ __forceinline__ float silu_times(float g, float u) {
+    const bool far = g < SILU_FAR;
+    const float e = expf(far ? 0.5f * g : -g);
+    return __fdividef(far ? g * e : g, far ? 1.0f : 1.0f + e) * (far ? u * e : u);
+}
+
+// The gated values of a chunk: lane 2i holds gate i, lane 2i + 1 up i; h[j] is row 2j in the even
+// lane, row 2j + 1 in the odd one.
+__device__ __forceinline__ void mx_gated(const float (&v)[32], float (&h)[16]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[2 * j] : v[2 * j + 1], 1);
+        h[j] = silu_times((lane & 1) ? got : v[2 * j], (lane & 1) ? v[2 * j + 1] : got);
+    }
+}
 
 // One chunk of an epilogue warp: rows row0 .. row0 + rows - 1 (rows <= 32) from accumulator
 // columns v, outputs from f0 on (this warp's: 32, gated 16).
@@ -186,14 +207,8 @@ __device__ __forceinline__ void mx_store_chunk(const MxArgs &p, const float (&v)
     T *out = reinterpret_cast<T *>(p.out) + (row0 + (GATED ? lane & 1 : 0)) * p.ld + f;
     const int64_t step = (GATED ? 2 : 1) * p.ld;
     float y[GATED ? 16 : 32];
-    if (GATED) {
-        // lane 2i holds gate i, lane 2i + 1 up i: the even lane takes row j, the odd one row j + 1
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[2 * j] : v[2 * j + 1], 1);
-            const float g = (lane & 1) ? got : v[2 * j], u = (lane & 1) ? v[2 * j + 1] : got;
-            y[j] = silu_fast(g) * u;
-        }
+    if constexpr (GATED) {
+        mx_gated(v, y);
     } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) y[j] = v[j];
@@ -222,13 +237,9 @@ __device__ __forceinline__ void mx_store_chunk_mxfp4(const MxArgs &p, const floa
     if (GATED) {
         float h[16];
         uint32_t m[16];
+        mx_gated(v, h);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[2 * j] : v[2 * j + 1], 1);
-            const float g = (lane & 1) ? got : v[2 * j], u = (lane & 1) ? v[2 * j + 1] : got;
-            h[j] = silu_fast(g) * u;
-            m[j] = __float_as_uint(h[j]) & 0x7fffffffu;
-        }
+        for (int j = 0; j < 16; ++j) m[j] = __float_as_uint(h[j]) & 0x7fffffffu;
 #pragma unroll
         for (int o = 2; o < 32; o <<= 1)
 #pragma unroll

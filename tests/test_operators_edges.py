@@ -105,3 +105,49 @@ def test_route_from_several_threads(ds4):
     assert wrong == [0] * len(state)
     for s, w in zip(state, want):
         assert torch.equal(s[1].topk_idx, w)
+
+
+# ------------------------------------------------------------------ gates far below zero
+@pytest.mark.gpu
+@pytest.mark.parametrize("low,high", [(-130, -84), (-86, -60), (-172, -130)])
+def test_gates_far_below_zero(ds4, low, high):
+    """silu(g) * u where e^-g is beyond 2^126 or infinite in fp32 and u is large: a normal value, not zero.
+    Rows of ones make the sums exact.  What is left, in half steps: the exponential 2, a quotient 4, a product 1.
+    Far below zero that is g e (2 + 1) over one (4), u e (2 + 1) and their product (1): 11; above, 1 + e (2 + 1),
+    the quotient (4) and the product (1): 8."""
+    rng = np.random.default_rng(-low)
+    N = 64
+    wg = np.zeros((N, 32))
+    for n in range(N):   # codes whose sum is a multiple of 0.5 in the range
+        left = rng.integers(2 * -high, 2 * -low + 1) / 2.0
+        for i in range(32):
+            v = ref.LADDER[ref.LADDER <= min(left, 6.0)][-1]
+            wg[n, i], left = -v, left - v
+        assert left == 0.0
+    wu = ref.LADDER[rng.integers(1, 8, (N, 32))] * 2.0 ** 110
+    wu[::3] *= -1
+    gc, gs = quantised(wg)
+    uc, us = quantised(wu)
+    ones_c = torch.full((3, 16), 0x22, dtype=torch.uint8)
+    ones_s = torch.full((3, 1), 127, dtype=torch.uint8)
+    g, u = ref.dequantize(gc, gs).sum(1), ref.dequantize(uc, us).sum(1)
+    assert g.max() <= high and g.min() >= low
+    want = np.tile(ref.silu(g) * u, (3, 1))
+    ex = ds4.Mxfp4Experts(1, N, 32, gated=True)
+    ex.load(*(torch.from_numpy(t).reshape(1, N, -1).cuda() for t in (gc, gs, uc, us)))
+    a = (ones_c.cuda(), ones_s.cuda(), None)
+    out = torch.empty(3, N, device="cuda")
+    ex.product(*a, out)
+    got = out.double().cpu().numpy()
+    normal = np.abs(want) >= 2.0 ** -126
+    assert normal.any()
+    assert (np.abs(got - want) <= 11 * ref.U24 * 1.001 * np.abs(want) + 2.0 ** -126 * ~normal).all()
+    codes, scales = torch.zeros(3, N // 2, dtype=torch.uint8, device="cuda"), torch.zeros(3, N // 32, dtype=torch.uint8, device="cuda")
+    ex.product(*a, codes, scales)
+    c, s = ds4.mxfp4_quantize(out)
+    assert torch.equal(c, codes) and torch.equal(s, scales)
+
+
+def quantised(w):
+    c, s = ref.quantize(w)
+    return np.ascontiguousarray(c), np.ascontiguousarray(s)
