@@ -90,7 +90,7 @@ struct MxCfg {
     static_assert(COLS <= 512, "tensor memory");
     static_assert(PER <= 2 && STAGES * PER >= 4, "a scale warp waits on every other pair of input tiles");
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
-    static_assert(NT % 16 == 0 && NT > BOX0 && BOX0 > BOX1 && BOX1 % 8 == 0, "row tiles");
+    static_assert(NT <= 255 && NT % 16 == 0 && NT > BOX0 && BOX0 > BOX1 && BOX1 % 8 == 0, "row tiles");
     static_assert((2 * STAGES + 5) * 8 + 16 + 32 + 4 * STAGES <= BAR_BYTES, "barrier area");
 };
 
@@ -128,6 +128,16 @@ __device__ __forceinline__ uint32_t mx_test(uint32_t bar, uint32_t parity) {
     return done;
 }
 
+constexpr int MX_MOST_ROWS = INT32_MAX - 255;   // a box of rows that begins at the last one ends within 31 bits
+
+// An expert's rows (up to 2^31 - 1) are cut into equal tiles of at most NT: how many tiles, and the
+// rows of each but the last, a multiple of 16.
+__host__ __device__ constexpr int mx_row_tiles(int rows, int NT) { return (int)(((uint32_t)rows + NT - 1) / NT); }
+__host__ __device__ constexpr int mx_tile_rows(int rows, int tiles, int NT) {
+    const int even = (int)((((uint32_t)rows + tiles - 1) / tiles + 15) & ~15u);
+    return even < NT ? even : NT;
+}
+
 struct MxTile {
     int e, m, row0, n;   // expert, weight row tile, first row of a, rows
 };
@@ -163,7 +173,7 @@ struct MxTiles {
             hi = lo + nt * MT;
             first = row_lo[e];
             last = row_hi[e];
-            per = min(NT, ((last - first + nt - 1) / nt + 15) & ~15);
+            per = mx_tile_rows(last - first, nt, NT);
         }
         MxTile x;
         x.e = e;
@@ -329,7 +339,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         int first, last;
         if (p.offsets && p.offsets[e] > p.offsets[e + 1]) decreasing = 1;
         mx_group(p, e, first, last);
-        S[e] = (last - first + C::NT - 1) / C::NT;
+        S[e] = mx_row_tiles(last - first, C::NT);
         S[SR_MAX_EXPERTS + 1 + e] = first;
         S[2 * (SR_MAX_EXPERTS + 1) + e] = last;
     }

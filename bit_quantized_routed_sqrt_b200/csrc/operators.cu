@@ -432,7 +432,7 @@ ds4moe_status ds4moe_mxfp4_product(ds4moe_mxfp4 *h, const uint8_t *a_codes_dev, 
     const ds4moe_mxfp4_config &g = h->cfg;
     if (injected("launch")) return fail(h, DS4MOE_ECUDA, "kernel launch failed (injected: DS4MOE_FAULT=launch)");
     if (!h->loaded) return fail(h, DS4MOE_ESTATE, "no weights loaded");
-    if (rows < 0) return fail(h, DS4MOE_EINVAL, "rows=%d is negative", rows);
+    if (rows < 0 || rows > MX_MOST_ROWS) return fail(h, DS4MOE_EINVAL, "rows=%d is not in 0 .. %d", rows, MX_MOST_ROWS);
     if (!float_type(out_type) && out_type != DS4MOE_MXFP4) return fail(h, DS4MOE_EINVAL, "unknown output type %d", out_type);
     if (out_type == DS4MOE_MXFP4 ? g.n_out % MX_BLOCK != 0 || ld != g.n_out || !out_scales_dev : out_scales_dev != nullptr)
         return fail(h, DS4MOE_EINVAL, "an MXFP4 output needs n_out %% 32 == 0, ld == n_out and scales; the others take no scales");

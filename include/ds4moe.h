@@ -340,7 +340,7 @@ void ds4moe_mxfp4_destroy(ds4moe_mxfp4 *h);
 ds4moe_status ds4moe_mxfp4_load(ds4moe_mxfp4 *h, const uint8_t *codes_dev, const uint8_t *scales_dev,
                                 const uint8_t *up_codes_dev, const uint8_t *up_scales_dev, void *cuda_stream);
 
-/* Products of rows with their experts' matrices: rows expert_offsets_dev[e] ..
+/* Products of rows (0 .. 2^31 - 256) with their experts' matrices: rows expert_offsets_dev[e] ..
  * expert_offsets_dev[e+1] - 1 of a (a_codes_dev [rows][K/2], 16-byte aligned; a_scales_dev
  * [rows][K/32]) belong to expert e; NULL offsets give every row to the one expert of a handle
  * with n_experts = 1.  out[r][n] = sum_k a[r][k] W[n][k], or silu(gate) * up, computed with

@@ -151,3 +151,20 @@ def test_gates_far_below_zero(ds4, low, high):
 def quantised(w):
     c, s = ref.quantize(w)
     return np.ascontiguousarray(c), np.ascontiguousarray(s)
+
+
+# ------------------------------------------------------------------ sizes next to 2^31
+@pytest.mark.gpu
+def test_product_refuses_more_rows_than_it_can_index(ds4):
+    """Row indexes past a tile's end stay below 2^31; the call is refused before any buffer is looked at."""
+    ex = ds4.Mxfp4Experts(1, 1, 32)
+    one = torch.full((1, 16), 0x22, dtype=torch.uint8, device="cuda")
+    scale = torch.full((1, 1), 127, dtype=torch.uint8, device="cuda")
+    ex.load(one, scale)
+    out = torch.zeros(1, 1, dtype=torch.bfloat16, device="cuda")
+    for rows in (-1, 2 ** 31 - 255, 2 ** 31 - 1):
+        with pytest.raises(ds4.Ds4MoeError, match="rows"):
+            ds4.ds4moe_mxfp4_product(ex.h, one, scale, rows, None, out, ds4.BF16, 1)
+    ex.product(one, scale, None, out)
+    ex.sync_status()
+    assert out.item() == 32.0
