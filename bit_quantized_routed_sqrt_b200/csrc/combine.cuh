@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(128) combine_shifted_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < PER; ++i) buf[warp][lane * (PER + 1) + i] = acc[i];
         __syncwarp();
-        const int c0 = g0 * PER, n = min(min(last, g0 + 32) * PER, p.H) - c0;
+        const int c0 = g0 * PER, n = min((min(last, g0 + 32) - g0) * PER, p.H - c0);   // last * PER can pass 2^31
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int c = 32 * i + lane;

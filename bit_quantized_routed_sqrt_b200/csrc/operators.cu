@@ -342,8 +342,8 @@ ds4moe_status ds4moe_combine(const void *o_dev, int32_t o_type, int64_t o_rows, 
     const int64_t per = 32 / size_of(o_type);   // columns of a 32-byte piece
     const bool vec = H % per == 0 && aligned32(o_dev) && H * size_of(o_type) % 32 == 0 && aligned32(y_dev) &&
                      H * size_of(y_type) % 16 == 0 && (!add_dev || aligned16(add_dev));
-    const int piece = 16 / size_of(o_type);
-    const RowSplit split = split_rows(T, vec ? H / per : (H + piece - 1) / piece, 4);
+    const int64_t piece = 16 / size_of(o_type);   // in 64 bits: H goes up to 2^31 - 1
+    const RowSplit split = split_rows(T, (int)(vec ? H / per : (H + piece - 1) / piece), 4);
     cudaError_t err = cudaSuccess;
     auto go = [&](auto kernel) { err = launch_ahead(kernel, T * split.segments, 128, 0, st, a, split); };
     auto with = [&](auto o) {

@@ -168,3 +168,16 @@ def test_product_refuses_more_rows_than_it_can_index(ds4):
     ex.product(one, scale, None, out)
     ex.sync_status()
     assert out.item() == 32.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [2 ** 31 - 1, 2 ** 31 - 7])
+def test_combine_of_the_widest_rows(ds4, H):
+    """Rows whose last piece of 16 bytes ends at or behind element 2^31."""
+    o = torch.ones(1, H, dtype=torch.bfloat16, device="cuda")
+    o[0, -9:] = torch.arange(9.0).bfloat16().cuda()
+    o[0, 5] = -2.0
+    y = torch.zeros(1, H, dtype=torch.bfloat16, device="cuda")
+    ds4.combine(o, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.full((1, 1), 2.0, device="cuda"), y)
+    o *= 2
+    assert torch.equal(y, o)
