@@ -60,10 +60,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Co
             float wt[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int r = j0 + j < p.k ? __ldg(inv + j0 + j) : -1;
+                const int r = j0 + j < p.k ? ld_input(inv + j0 + j) : -1;
                 const bool on = r >= 0 && r < p.o_rows;
-                wt[j] = on ? __ldg(w + j0 + j) : 0.0f;
-                if (on) ld_stream_v8(o + (size_t)r * p.H + g * PER, u[j]);
+                wt[j] = on ? ld_input(w + j0 + j) : 0.0f;
+                if (on) ld_once_v8(o + (size_t)r * p.H + g * PER, u[j]);
                 else
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[j][i] = 0u;
@@ -121,14 +121,14 @@ __global__ void __launch_bounds__(128) combine_shifted_kernel(const __grid_const
             uint32_t m[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int r = j0 + j < p.k ? __ldg(inv + j0 + j) : -1;
+                const int r = j0 + j < p.k ? ld_input(inv + j0 + j) : -1;
                 const bool on = r >= 0 && r < p.o_rows;
                 const uintptr_t at = base + ((size_t)(on ? r : 0) * p.H + (size_t)g * PER) * sizeof(TO), piece = at & ~(uintptr_t)15;
                 m[j] = (uint32_t)at & 15u;
-                wt[j] = on ? __ldg(w + j0 + j) : 0.0f;
+                wt[j] = on ? ld_input(w + j0 + j) : 0.0f;
                 lo[j] = hi[j] = make_uint4(0, 0, 0, 0);
-                if (on && g < last && piece < end) lo[j] = ld_stream_v4(reinterpret_cast<const void *>(piece));
-                if (on && g < last && m[j] && piece + 16 < end) hi[j] = __ldg(reinterpret_cast<const uint4 *>(piece + 16));
+                if (on && g < last && piece < end) lo[j] = ld_once_v4(reinterpret_cast<const void *>(piece));
+                if (on && g < last && m[j] && piece + 16 < end) hi[j] = ld_input(reinterpret_cast<const uint4 *>(piece + 16));
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

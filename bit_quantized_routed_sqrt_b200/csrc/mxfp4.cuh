@@ -50,9 +50,51 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// Loads of a kernel's inputs.  They are ordinary loads: the read-only path (ld.global.nc, __ldg) is
+// for data that nothing writes while the kernel lives, and a kernel here is alive while the one
+// before it writes them (see next_kernel_may_start).  A load without volatile may move, but not
+// ahead of the wait that its address comes from (after_wait).
+__device__ __forceinline__ int ld_input(const int *p) {
+    int v;
+    asm("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_input(const uint32_t *p) {
+    uint32_t v;
+    asm("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float ld_input(const float *p) {
+    float v;
+    asm("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_input(const uint8_t *p) {
+    uint32_t v;
+    asm("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_input(const uint2 *p) {
+    uint2 v;
+    asm("ld.global.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_input(const uint4 *p) {
+    uint4 v;
+    asm("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 ld_once_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 // 32 bytes at once (32-byte aligned): a lane's load is a whole sector.
-__device__ __forceinline__ void ld_stream_v8(const void *p, uint32_t (&r)[8]) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+__device__ __forceinline__ void ld_once_v8(const void *p, uint32_t (&r)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "l"(p));
 }
@@ -70,7 +112,7 @@ __device__ __forceinline__ void load_row(const T *p, float (&v)[N]) {
 #pragma unroll
         for (int i = 0; i < N / PER; ++i) {
             uint32_t u[8];
-            ld_stream_v8(p + i * PER, u);
+            ld_once_v8(p + i * PER, u);
             const T *t = reinterpret_cast<const T *>(u);
 #pragma unroll
             for (int j = 0; j < PER; ++j) v[i * PER + j] = to_f32<T>(t[j]);
@@ -104,8 +146,8 @@ __device__ __forceinline__ void store_row(T *p, const float (&v)[N]) {
 // product 17.5 -> 15.7 us, the routing of 2048 tokens (two kernels) 12.3 -> 10.0.
 __device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// A pointer whose read-only loads (which the compiler may move past other memory operations)
-// cannot move ahead of that wait.
+// A pointer whose loads (those of ld_input may move past other memory operations) cannot move
+// ahead of that wait.
 template <class T>
 __device__ __forceinline__ T *after_wait(T *p) {
     asm volatile("" : "+l"(p)::"memory");
@@ -166,7 +208,7 @@ __global__ void __launch_bounds__(128) mxfp4_quantize_kernel(const T *x, int64_t
         } else {
 #pragma unroll 4
             for (int j = 0; j < k; ++j) {
-                const int p = __ldg(inv_pos + (size_t)r * k + j);
+                const int p = ld_input(inv_pos + (size_t)r * k + j);
                 if (p < 0 || p >= out_rows) continue;
                 *reinterpret_cast<uint2 *>(codes + (size_t)p * (K / 2) + code_at) = c;
                 if ((g & 1) == 0) scales[(size_t)p * (K / MX_BLOCK) + scale_at] = (uint8_t)s;
@@ -191,8 +233,8 @@ __global__ void __launch_bounds__(128) mxfp4_dequantize_kernel(const uint8_t *co
     split.place(r, first, last);
 #pragma unroll 2
     for (int g = first + threadIdx.x; g < last; g += blockDim.x) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes + (size_t)r * (K / 2)) + g);
-        const float s = e8m0_value(__ldg(scales + (size_t)r * (K / MX_BLOCK) + (g >> 1)));
+        const uint2 c = ld_input(reinterpret_cast<const uint2 *>(codes + (size_t)r * (K / 2)) + g);
+        const float s = e8m0_value(ld_input(scales + (size_t)r * (K / MX_BLOCK) + (g >> 1)));
         float v[16];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
                 if (32 * j >= x.n) break;
                 const uint8_t *src = a_scales + (size_t)(x.row0 + min(32 * j + lane, x.n - 1)) * kb + pt * 16;
                 if (aligned) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src));
+                    const uint4 u = ld_input(reinterpret_cast<const uint4 *>(src));
                     nxt[j][0] = u.x; nxt[j][1] = u.y; nxt[j][2] = u.z; nxt[j][3] = u.w;
                 } else {
                     // aligned words that hold any of the row's bytes, shifted; bytes past K are 0
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
                     const int off = (int)((uintptr_t)src & 3);
                     uint32_t v[5];
 #pragma unroll
-                    for (int i = 0; i < 5; ++i) v[i] = 4 * i < off + min(left, 16) ? __ldg(word + i) : 0u;
+                    for (int i = 0; i < 5; ++i) v[i] = 4 * i < off + min(left, 16) ? ld_input(word + i) : 0u;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int valid = left - 4 * i;

@@ -249,11 +249,11 @@ struct LaneLogits {
             if constexpr (BYTES % 16 == 0) {
 #pragma unroll
                 for (int i = 0; i < BYTES / 16; ++i) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+                    const uint4 u = ld_input(reinterpret_cast<const uint4 *>(src) + i);
                     w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
                 }
             } else {
-                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
+                const uint2 u = ld_input(reinterpret_cast<const uint2 *>(src));
                 w[0] = u.x; w[1] = u.y;
             }
         } else {
