@@ -25,6 +25,7 @@ ROUTE_STATIC_MAX_TOKENS = 256
 F32, BF16, F16, MXFP4 = 0, 1, 2, 3
 SCORES = {"softmax": 0, "sigmoid": 1, "sqrt_softplus": 2}
 GROUP_SCORES = {"max": 0, "top2": 1}
+INT_MAX = 2 ** 31 - 1
 
 STATUS = {0: "DS4MOE_OK", 1: "DS4MOE_EINVAL", 2: "DS4MOE_ENOMEM", 3: "DS4MOE_ECUDA",
           4: "DS4MOE_ESTATE", 5: "DS4MOE_ETIMEOUT", 6: "DS4MOE_EDEVICE"}
@@ -242,6 +243,12 @@ def _rows_of(t, what: str):
     return rows, width, ld
 
 
+def _fits(sizes: int):
+    """Refuses sizes that the C calls' 32-bit arguments cannot hold; sizes: all of them, or-ed."""
+    if sizes > INT_MAX:
+        raise ValueError("sizes must be at most 2^31 - 1")
+
+
 def _flat(t, dtype: str, n: int, what: str, device):
     """The address of a contiguous tensor of n elements of the type on the device (None stays None)."""
     if t is None:
@@ -313,6 +320,7 @@ class Router:
         device = _device_of(logits, "logits")
         T, E, ld = _rows_of(logits, "logits")
         code = _type_of(logits, "logits")
+        _fits(T)
         if E != self.cfg.n_experts:
             raise ValueError("logits have %d columns for %d experts" % (E, self.cfg.n_experts))
         bias_at = _flat(bias, "float32", E, "bias", device)   # bias itself stays alive to the call
@@ -340,8 +348,10 @@ def mxfp4_quantize(x, inv_pos=None, codes=None, scales=None):
         k = inv_pos.shape[1]
         places = _flat(inv_pos, "int32", rows * k, "inv_pos", device)
     if codes is None:
+        _fits(rows * k | K)
         codes = _torch.empty((rows * k, K // 2), dtype=_torch.uint8, device=device)
     out_rows = codes.shape[0]
+    _fits(rows | K | k | out_rows)
     if scales is None:
         scales = _torch.empty((out_rows, K // 32), dtype=_torch.uint8, device=device)
     _check(_run(device, lib.ds4moe_mxfp4_quantize, x.data_ptr(), code, ld, rows, K, places, k, out_rows,
@@ -356,6 +366,7 @@ def mxfp4_dequantize(codes, scales, out=None):
     device = _device_of(codes, "codes")
     rows, half, _ = _rows_of(codes, "codes")
     K = 2 * half
+    _fits(rows | K)
     if out is None:
         out = _torch.empty((rows, K), dtype=_torch.bfloat16, device=device)
     r, w, ld = _rows_of(out, "out")
@@ -377,6 +388,7 @@ def combine(o, inv_pos, topk_w, y=None, add=None):
     if topk_w.dim() != 2:
         raise ValueError("topk_w must be [T, k]")
     T, k = topk_w.shape
+    _fits(T | k | H)
     if y is None:
         y = _torch.empty((T, H), dtype=_torch.float32, device=device)
     for t, what in ((y, "y"), (add, "add")):
@@ -438,6 +450,7 @@ class Mxfp4Experts:
         strided; or uint8 [rows, n_out / 2] with out_scales uint8 [rows, n_out / 32] for MXFP4."""
         device = self._device_of(a_codes, "a_codes")
         rows, half, _ = _rows_of(a_codes, "a_codes")
+        _fits(rows)
         if half * 2 != self.n_in:
             raise ValueError("a_codes has rows of %d inputs, the experts take %d" % (half * 2, self.n_in))
         if out is None:

@@ -181,3 +181,63 @@ def test_combine_of_the_widest_rows(ds4, H):
     ds4.combine(o, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.full((1, 1), 2.0, device="cuda"), y)
     o *= 2
     assert torch.equal(y, o)
+
+
+class Claims:
+    """A tensor that claims a shape and to be on the GPU; no refused call may look at its memory."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=None):
+        self.shape, self.dtype, self.device = shape, dtype or torch.bfloat16, torch.device("cuda", 0)
+
+    def stride(self):
+        return (self.shape[1], 1)
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape[0] * self.shape[1]
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+def test_sizes_beyond_32_bits_are_refused(ds4_cpu, monkeypatch):
+    """A size past 2^31 - 1 would reach the library as another one."""
+    ds4 = ds4_cpu
+    monkeypatch.setattr(ds4, "_run", lambda *a: pytest.fail("the library was called"))
+    big, u8, i32, f32 = 2 ** 32, torch.uint8, torch.int32, torch.float32
+    one = Claims(1, 1, dtype=f32)
+    for call in (lambda: ds4.Router(1, 1).route(Claims(big + 3, 1)),
+                 lambda: ds4.mxfp4_quantize(Claims(1, big + 32)),
+                 lambda: ds4.mxfp4_quantize(Claims(big + 1, 32)),
+                 lambda: ds4.mxfp4_quantize(Claims(1, 32), Claims(1, big + 1, dtype=i32)),
+                 lambda: ds4.mxfp4_quantize(Claims(1, 32), None, Claims(big + 1, 16, dtype=u8), Claims(big + 1, 1, dtype=u8)),
+                 lambda: ds4.mxfp4_dequantize(Claims(big + 1, 16, dtype=u8), Claims(big + 1, 1, dtype=u8), Claims(big + 1, 32)),
+                 lambda: ds4.mxfp4_dequantize(Claims(1, 2 ** 31 - 16, dtype=u8), Claims(1, 2 ** 27 - 1, dtype=u8), Claims(1, 2 ** 32 - 32)),
+                 lambda: ds4.combine(Claims(1, big + 8), Claims(1, 1, dtype=i32), one, Claims(1, big + 8)),
+                 lambda: ds4.combine(Claims(1, 8), Claims(big + 1, 1, dtype=i32), Claims(big + 1, 1, dtype=f32), Claims(big + 1, 8)),
+                 lambda: experts(ds4).product(Claims(big + 1, 16, dtype=u8), Claims(big + 1, 1, dtype=u8), None, Claims(big + 1, 1)),
+                 lambda: ds4.combine(Claims(1, 8), Claims(1, big + 1, dtype=i32), Claims(1, big + 1, dtype=f32), Claims(1, 8))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
+
+def experts(ds4):
+    """A handle's object without the handle."""
+    e = object.__new__(ds4.Mxfp4Experts)
+    e.h, e.device, e.n_experts, e.n_out, e.n_in, e.gated = None, 0, 1, 1, 32, False
+    return e
+
+
+@pytest.fixture(scope="module")
+def ds4_cpu():
+    import __graft_entry__
+    __graft_entry__.build_library()
+    import bit_quantized_routed_sqrt_b200 as m
+    m._bind_torch()
+    return m
