@@ -447,14 +447,16 @@ class Mxfp4Experts:
     def product(self, a_codes, a_scales, offsets=None, out=None, out_scales=None):
         """Rows of a [rows, n_in] in MXFP4, grouped by offsets int32 [E + 1] (None for one expert), times their
         experts' matrices.  out: [rows, n_out] of float32, bfloat16 (where it is not given) or float16, rows may be
-        strided; or uint8 [rows, n_out / 2] with out_scales uint8 [rows, n_out / 32] for MXFP4."""
+        strided; or, with out_scales uint8 [rows, n_out / 32], the codes of MXFP4, uint8 [rows, n_out / 2] (made
+        where they are not given).  Returns out."""
         device = self._device_of(a_codes, "a_codes")
         rows, half, _ = _rows_of(a_codes, "a_codes")
         _fits(rows)
         if half * 2 != self.n_in:
             raise ValueError("a_codes has rows of %d inputs, the experts take %d" % (half * 2, self.n_in))
         if out is None:
-            out = _torch.empty((rows, self.n_out), dtype=_torch.bfloat16, device=device)
+            out = _torch.empty((rows, self.n_out if out_scales is None else self.n_out // 2),
+                               dtype=_torch.bfloat16 if out_scales is None else _torch.uint8, device=device)
         if out_scales is not None:
             to, ld, code = _flat(out, "uint8", rows * (self.n_out // 2), "out", device), self.n_out, MXFP4
         else:

@@ -10,7 +10,7 @@ import pytest
 import operator_refs as ref
 
 torch = pytest.importorskip("torch")
-from test_operators import TYPES, check_route, ds4, gen  # noqa: E402, F401  (ds4: the fixture)
+from test_operators import TYPES, check_route, ds4, gen, make, mx_random  # noqa: E402, F401  (ds4: the fixture)
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -241,3 +241,19 @@ def ds4_cpu():
     import bit_quantized_routed_sqrt_b200 as m
     m._bind_torch()
     return m
+
+
+# ------------------------------------------------------------------ the binding
+@pytest.mark.gpu
+def test_product_makes_mxfp4_codes_for_given_scales(ds4):
+    ex, _ = make(ds4, 3, 64, 96, True, 40)
+    codes, scales = (t.cuda() for t in mx_random((9, 96), gen(41)))
+    off = torch.tensor([0, 4, 4, 9], dtype=torch.int32, device="cuda")
+    want, want_s = torch.zeros(9, 32, dtype=torch.uint8, device="cuda"), torch.zeros(9, 2, dtype=torch.uint8, device="cuda")
+    ex.product(codes, scales, off, want, want_s)
+    got_s = torch.zeros_like(want_s)
+    got = ex.product(codes, scales, off, out_scales=got_s)
+    ex.sync_status()
+    assert torch.equal(got, want) and torch.equal(got_s, want_s)
+    with pytest.raises(ValueError, match="out_scales"):
+        ex.product(codes, scales, off, out_scales=got_s[:8])
