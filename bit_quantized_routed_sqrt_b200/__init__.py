@@ -361,8 +361,9 @@ def mxfp4_quantize(x, inv_pos=None, codes=None, scales=None):
 
 
 def mxfp4_dequantize(codes, scales, out=None):
-    """The values of MXFP4 rows, in out (float32, bfloat16 or float16 [rows, K]; bfloat16 where it is not given,
-    which holds every value but 2^-127 * 0.5 exactly)."""
+    """The values of MXFP4 rows, in out (float32, bfloat16 or float16 [rows, K]; bfloat16 where it is not given:
+    it and float32 hold every value exactly, but those of 2^128 and above, at scale bytes 253 and 254, are
+    infinite)."""
     device = _device_of(codes, "codes")
     rows, half, _ = _rows_of(codes, "codes")
     K = 2 * half

@@ -117,7 +117,7 @@ bool router_ok(const ds4moe_router *r) {
            r->group_score >= DS4MOE_GROUP_MAX && r->group_score <= DS4MOE_GROUP_TOP2 &&
            (r->renormalise == 0 || r->renormalise == 1) && r->scale - r->scale == 0.0f;
 }
-// Tokens a block: about four blocks an SM where there are tokens for it.
+// Tokens a block: up to four blocks an SM where there are tokens for it (three are resident at once).
 int route_block(int T) {
     int TB = T <= 64 ? 64 : SR_MIN_BLOCK;
     while (TB < SR_MAX_BLOCK && T / TB > 592) TB *= 2;
@@ -167,9 +167,12 @@ ds4moe_status run_product(ds4moe_mxfp4 *h, const MxArgs &a, cudaStream_t st) {
 // stage, elsewhere.  Measured (us, 32 / 192 rows a tile; 64 experts, 4096 x 4096, by the mean rows
 // an expert): 8 rows 106 / 106, 24 106 / 107, 32 106 / 108, 40 115 / 109; one row each of 8 of 256
 // experts (gated, 2048 x 4096) 17.6 / 22.3, 40 rows of 32 experts 21.9 / 26.0, one expert with 16
-// rows 9.2 / 10.4 (all before kernels were launched ahead).  Two steps a stage (half the barriers)
-// took one row of one expert from 10.4 to 8.9 us; with wide tiles they leave three stages of 128 rows or two of 192: 94 and 91 against
-// 90 us at 8191 x 4096 x 4096.
+// rows 9.2 / 10.4 (all before kernels were launched ahead; now 24, 32 and 40 rows each 89, 92 and
+// 93).  These loads are even.  The rule sees the mean over all experts, idle ones included, so many
+// rows of few among many experts get narrow tiles, and their weights come from L2 once for each 32
+// rows: 4096 rows of 20 of 256 experts take 101 us, of 20 of 20 experts (wide tiles) 55.  Two steps
+// a stage (half the barriers) took one row of one expert from 10.4 to 8.9 us; with wide tiles they
+// leave three stages of 128 rows or two of 192: 94 and 91 against 90 us at 8191 x 4096 x 4096.
 template <bool GATED>
 using FewRows = MxCfg<32, 16, 8, 4, 2, GATED>;
 template <bool GATED>

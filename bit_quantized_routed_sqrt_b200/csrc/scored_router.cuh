@@ -2,11 +2,13 @@
 // bias on the choice, groups, top-k, renormalised weights, and the token -> expert permutation.
 //
 // s = softmax(l), sigmoid(l) or sqrt(log(1 + e^l)); the choice goes by s + bias (without a bias by
-// l, which orders alike), the weight is that of s.  A warp per token; what bounds it is the
-// instructions of a token, not its bytes: 700 of them at 256 experts with a bias (300 the scores,
-// 160 the sort and the k picks, 120 the weights), 460 without, so 65536 tokens take 76 us for the
-// choice and 88 with the permutation where their 78 MB take 12 at a copy's rate.  Scores in fp64
-// throughout took 520.  A single token takes 4.4 us of the GPU.
+// l, which orders alike), the weight is that of s.  A warp per token.  65536 tokens of 256 experts
+// with a bias take 76 us for the choice and 87 with the permutation where their 78 MB take 12 at a
+// copy's rate.  700 instructions a token (300 the scores, 160 the sort and the k picks, 120 the
+// weights; 460 without a bias) are 39 us of issue.  In the rest, not measured apart: three blocks an
+// SM are resident, so the last of 512 run in a second turn; registers spill (72 bytes stored a thread
+// in this build, 136 for rows that are not aligned pieces); 31% of the warps' places are active.
+// Scores in fp64 throughout took 520.  A single token takes 4.4 us of the GPU.
 #pragma once
 #include "combine.cuh"
 #include "scan.cuh"
@@ -16,7 +18,7 @@ namespace ds4 {
 constexpr int SR_MAX_TOPK = 32;
 constexpr int SR_MAX_GROUPS = 32;
 constexpr int SR_MIN_BLOCK = 32, SR_MAX_BLOCK = 256;     // tokens a CTA
-constexpr int SR_WARPS = 8, SR_MAX_WARPS = 16;           // warps a CTA (a lone CTA: up to 16)
+constexpr int SR_WARPS = 8, SR_MAX_WARPS = 16;           // warps a CTA (up to 16 where there are at most 148 CTAs)
 constexpr int SR_DIRECT = 256;                           // blocks whose counts every CTA adds up itself
 constexpr int SR_PERMUTE_THREADS = 512;
 // Dynamic shared memory that a launch may have without leave: 48 KB less what the kernel has
@@ -213,7 +215,7 @@ __device__ __forceinline__ float log1p_unit(float t, float rcp_2_t) {
     return 2.0f * fmaf(s * q, z, z);
 }
 
-// Sorts v descending (odd-even merges).
+// Sorts v descending (Batcher's odd-even merge sort).
 template <int N>
 __device__ __forceinline__ void sort_network(uint32_t (&v)[N]) {
 #pragma unroll
@@ -468,6 +470,9 @@ __device__ __forceinline__ float exp_diff(float x, float y, float half) {   // e
 // Renormalised, scores count up to a factor common to the token, exp(-m) (sqrt-softplus:
 // exp(-m / 2)) with m the largest chosen logit (softmax) or that where it is negative and 0
 // elsewhere: tokens whose scores all underflow have weights too.
+// In half steps of fp32 (expf and each approximate function 2, a quotient by __fdividef 4) a softmax
+// score is off by at most 4, a sigmoid score 11, a sqrt-softplus score 14; the weight by that, what
+// the sum has (the same and 5 for up to 32 terms), the quotient's 4 and the scale's 1: 38 at most.
 template <int NPL, class T, bool VEC>
 __device__ __forceinline__ float scored_weight(const ScoredArgs &p, int64_t t, const LaneLogits<NPL, T, VEC> &logits, int e) {
     const bool on = e >= 0;

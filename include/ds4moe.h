@@ -280,8 +280,8 @@ size_t ds4moe_route_logits_workspace(const ds4moe_router *r, int32_t T);
  *  groups with the largest choice values, in descending order; ties go to the lower index.
  *  Choice values are compared as fp64 evaluations of them; without a bias experts are
  *  compared by their logits, which order as their scores do.
- *  Weights: w_j = scale * s_j, or scale * s_j / sum_i s_i; the quotient is that of the exact
- *  scores, also where they underflow.
+ *  Weights, in fp32: w_j = scale * s_j, where a score below 2^-126 may count as zero, or
+ *  scale * s_j / sum_i s_i; the quotient is that of the exact scores, also where they underflow.
  *  A logit of -inf or NaN (or a bias that makes the choice value so) leaves its expert out;
  *  +inf counts as the largest finite fp32 value.  Where fewer than k experts are left, the
  *  remaining slots get index -1 and weight 0 and take no place in the permutation.
