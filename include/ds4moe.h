@@ -282,7 +282,7 @@ size_t ds4moe_route_logits_workspace(const ds4moe_router *r, int32_t T);
  *  compared by their logits, which order as their scores do.
  *  Weights, in fp32: w_j = scale * s_j, where a score below 2^-126 may count as zero, or
  *  scale * s_j / sum_i s_i; the quotient is that of the exact scores, also where they underflow.
- *  A logit of -inf or NaN (or a bias that makes the choice value so) leaves its expert out;
+ *  Zeros of both signs are equal.  A logit of -inf or NaN (or a bias that makes the choice value so) leaves its expert out;
  *  +inf counts as the largest finite fp32 value.  Where fewer than k experts are left, the
  *  remaining slots get index -1 and weight 0 and take no place in the permutation.
  *  Outputs: topk_idx_dev, topk_w_dev [T][k]; the permutation as in ds4moe_route, each of its
@@ -356,7 +356,9 @@ ds4moe_status ds4moe_mxfp4_product(ds4moe_mxfp4 *h, const uint8_t *a_codes_dev, 
                                    const int32_t *expert_offsets_dev, void *out_dev, int32_t out_type, int64_t ld,
                                    uint8_t *out_scales_dev, void *cuda_stream);
 
-/* Synchronise the last stream the handle used and return its sticky device status; clears it. */
+/* Synchronise the last stream the handle used and return its sticky device status; clears it.
+ * What runs elsewhere (calls on other streams, replays of a captured graph) is in it once the
+ * caller has waited for that. */
 ds4moe_status ds4moe_mxfp4_sync_status(ds4moe_mxfp4 *h);
 /* One-line detail of the handle's last error, owned by the handle ("" if none). */
 const char *ds4moe_mxfp4_last_error(const ds4moe_mxfp4 *h);
